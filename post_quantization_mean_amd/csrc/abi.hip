@@ -8,14 +8,16 @@
 #include <mutex>
 
 #include "awq.h"
+#include "abi_status.h"
 #include "internal.h"
 #include "variants.h"
 #include "w4a16.h"
 #include "block.h"
 
+namespace awq {
 namespace {
-
 thread_local char g_err[512] = "";
+}
 
 int fail(int status, const char* fmt, ...) {
   va_list ap;
@@ -33,6 +35,15 @@ int ok() {
 int hip_fail(hipError_t e, const char* where) {
   return fail(AWQ_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
+
+static const char* last_error() { return g_err; }
+}  // namespace awq
+
+namespace {
+
+using awq::fail;
+using awq::hip_fail;
+using awq::ok;
 
 size_t esize(int dtype) { return dtype == AWQ_DTYPE_BF16 ? 2 : 4; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -289,7 +300,7 @@ const char* awq_status_string(int status) {
   }
 }
 
-const char* awq_last_error(void) { return g_err; }
+const char* awq_last_error(void) { return awq::last_error(); }
 
 size_t awq_act_stats_workspace_bytes(int dtype, int64_t n_tokens, int64_t d_in) {
   if ((dtype != AWQ_DTYPE_BF16 && dtype != AWQ_DTYPE_F32) || n_tokens <= 0 || d_in <= 0 ||
@@ -686,7 +697,7 @@ int awq_w4a16_gemm(const void* x, int64_t ld_x, int x_dtype, const uint8_t* code
   if (!x || !codes || !steps_f16 || !zeros_u4 || !y) return fail(AWQ_ERR_NULL, "a required pointer is NULL");
   if (ld_x < d_in) return fail(AWQ_ERR_ARG, "ld_x %lld < d_in %lld", (long long)ld_x, (long long)d_in);
   if (ld_y < d_out) return fail(AWQ_ERR_ARG, "ld_y %lld < d_out %lld", (long long)ld_y, (long long)d_out);
-  if (ld_x % 8 || !aligned(x, 16)) return fail(AWQ_ERR_UNSUPPORTED, "x must be 16-byte aligned with ld_x % 8 == 0");
+  if (ld_x % 8 || !aligned(x, 16)) return fail(AWQ_ERR_UNSUPPORTED, "x must be 16-byte aligned with ld_x %% 8 == 0");
   if (!aligned(codes, 16) || !aligned(steps_f16, 2))
     return fail(AWQ_ERR_UNSUPPORTED, "codes must be 16-byte and steps_f16 2-byte aligned");
   if (!aligned(y, y_dtype == AWQ_DTYPE_F32 ? 4 : 2)) return fail(AWQ_ERR_UNSUPPORTED, "y is not element-aligned");
