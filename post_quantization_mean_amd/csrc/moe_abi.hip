@@ -156,6 +156,9 @@ int check_grouped(const char* x_name, const void* x, int64_t ld_x, int64_t x_wid
   if (ld_x > 0x3FFFFF || d_in > 0x3FFF80 || d_out > 0x3FFFFF)
     return fail(AWQ_ERR_UNSUPPORTED, "%s pitch %lld, d_in %lld or d_out %lld too large for 32-bit tile offsets", x_name,
                 (ll)ld_x, (ll)d_in, (ll)d_out);
+  if (d_out > 0x7FFFFFFF / (d_in / 2))
+    return fail(AWQ_ERR_UNSUPPORTED, "an expert of %lld x %lld weights is too large for 32-bit offsets", (ll)d_out,
+                (ll)d_in);
   return AWQ_OK;
 }
 

@@ -15,10 +15,9 @@
 // assignment of the contraction index to (lane group, element) works as long as A and B use the same
 // one; here lane group kq of sub-step t of a 128-wide group holds k = 32 kq + 8 t + e, so that a lane's
 // codes for a whole group are one 16-byte load (32 nibbles) and its activations 64 contiguous bytes.
-#include <type_traits>
-
 #include "w4a16.h"
 #include "w4a16_device.h"
+#include "w4a16_tile.h"
 
 namespace awq {
 namespace {
@@ -426,18 +425,9 @@ __global__ __launch_bounds__(kThreads, 2) void w4a16_big_kernel(const uint16_t* 
   }
 }
 
-// Prefill at scale (thousands of tokens): the error GEMM's tiling with the weight operand produced in
-// LDS. A block computes 256 tokens x 256 output rows; four waves as 2 x 2, each 128 x 128 as 4 x 4
-// accumulators of v_mfma_f32_32x32x16_{bf16,f16}. A K step is 64 inputs: the activations (256 rows
-// x 128 bytes) move global -> LDS by buffer DMA, and the weights are dequantized by the block's
-// threads, one output row each (64 codes, the group's float16 step and zero point), into the same
-// swizzled LDS layout, so every weight is dequantized once per 256 tokens and read by two waves.
-// Two LDS stages: the activations of step kt+2 are loaded into the stage step kt has just freed, and
-// its weights dequantized there, spread over the four sub-steps that follow (half a chunk of eight
-// weights per four MFMAs); each step's codes are requested a step before their dequantization
-// begins. Tiles in the super-block order of the error GEMM (one block per compute unit at a time).
-constexpr int kTileTok = 256, kTileRows = 256, kTileKB = 128;
-constexpr int kTileStage = (kTileTok + kTileRows) * kTileKB;  // 64 KiB
+// Prefill at scale (thousands of tokens): 256 tokens x 256 output rows per block, weights dequantized into
+// LDS once per 256 tokens (w4a16_tile.h). Tiles in the super-block order of the error GEMM (one block per
+// compute unit at a time).
 constexpr int64_t kTileMinTokens = 1024;
 
 template <int KIND, typename OutT>
@@ -445,7 +435,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
 void w4a16_tile_kernel(const uint16_t* __restrict__ x, int64_t ld_x, const uint8_t* __restrict__ codes,
                        const uint16_t* __restrict__ steps, const uint8_t* __restrict__ zeros, int n_tokens,
                        int d_in, int d_out, OutT* __restrict__ y, int64_t ld_y, int tiles_m, int tiles_n) {
-  constexpr int FM = 4, FN = 4, NR = 8, KB = kTileKB, BM = kTileTok;
+  constexpr int FM = 4, FN = 4;
   __shared__ __attribute__((aligned(1024))) char lds[2 * kTileStage];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -454,24 +444,10 @@ void w4a16_tile_kernel(const uint16_t* __restrict__ x, int64_t ld_x, const uint8
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * kTileTok, n0 = (int64_t)tn * kTileRows;
   const int G = d_in / kGroup, GZ = (G + 1) / 2;
-  const int k_steps = d_in / 64;  // >= 2
 
-  // activations: DMA load j of wave w covers token rows (4 j + w) * 8 .. + 7 (as the error GEMM's A);
-  // tokens past the end lie outside the descriptor's range and read as zero (their rows are not stored)
   const int lda_bytes = (int)ld_x * 2;
   const int rows_a = (int)min((int64_t)kTileTok, (int64_t)n_tokens - m0);
   const i32x4 ra = make_rsrc(x + m0 * ld_x, (uint32_t)((rows_a - 1) * lda_bytes + d_in * 2));
-  int voff_a[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int row = (4 * j + wave) * 8 + (lane >> 3);
-    voff_a[j] = row * lda_bytes + (((lane & 7) ^ swz(row)) << 4);
-  }
-  const uint32_t lds_base = __builtin_amdgcn_readfirstlane(lds_address(lds));
-  auto dma_a = [&](uint32_t stage, int j, int kstep) {
-    dma_load16(ra, __builtin_amdgcn_readfirstlane(stage + (4 * j + wave) * 8 * KB), voff_a[j], kstep * KB);
-  };
-
   // weights: thread t dequantizes output row n0 + t; rows past d_out read zero codes, steps and zero
   // points through range-checked descriptors (the row offset is in the range-checked per-lane offset)
   const int vrows = (int)max((int64_t)0, min((int64_t)kTileRows, (int64_t)d_out - n0));
@@ -483,170 +459,12 @@ void w4a16_tile_kernel(const uint16_t* __restrict__ x, int64_t ld_x, const uint8
   const __amdgpu_buffer_rsrc_t zr = __builtin_amdgcn_make_buffer_rsrc((void*)(zeros + r0 * GZ), (short)0,
                                                                      vrows * GZ, 0x00020000);
   const int c_off = tid * (d_in / 2), s_off = tid * G * 2, z_off = tid * GZ;
-  uint4 cw[2][2];           // codes of two K steps (64 each) in flight / in use
-  uint32_t sw[2], zw[2];    // their group's raw float16 step and zero-point byte
-  auto load_codes = [&](int set, int kstep) {
-    cw[set][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(cr, c_off, kstep * 32, 0));
-    cw[set][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(cr, c_off + 16, kstep * 32, 0));
-    sw[set] = __builtin_amdgcn_raw_buffer_load_b16(sr, s_off, (kstep >> 1) * 2, 0);
-    zw[set] = __builtin_amdgcn_raw_buffer_load_b8(zr, z_off, kstep >> 2, 0);
-  };
-  // chunk c (inputs 8 c .. 8 c + 7 of the step) of this thread's row, into the stage's weight rows
-  const uint32_t brow = BM * KB + tid * KB;
-  auto code_word = [&](int set, int c) -> uint32_t {
-    const uint4 u = cw[set][c >> 2];
-    return (c & 3) == 0 ? u.x : (c & 3) == 1 ? u.y : (c & 3) == 2 ? u.z : u.w;
-  };
-  float gst[2], gnzs[2];  // the group's step and -zero * step for the step whose codes are in set 0 / 1
-  auto params = [&](int set, int kstep) { tile_group_params(sw[set], zw[set], kstep >> 1, gst[set], gnzs[set]); };
-  auto dequant_chunk = [&](char* stage, int set, int c) {
-    *reinterpret_cast<uint4*>(stage + brow + ((c ^ swz(tid)) << 4)) =
-        dequant8_bytes<KIND>(code_word(set, c), gst[set], gnzs[set]);
-  };
-  // the same as a pipeline of eight parts of at most four VALU instructions, one part after each MFMA
-  // (a chunk per eight MFMAs): the parts' dependency chains span several MFMAs instead of stalling
-  // the issue of the next one; part 7 writes the chunk to LDS
-  uint32_t dlo = 0, dhi = 0, dq[4];
-  float dv[4];
-  auto dequant_part = [&](char* stage, int set, int c, int m) {
-    const float st = gst[set], nzs = gnzs[set];
-    if (m == 0) {
-      const uint32_t wd = code_word(set, c);
-      dlo = wd & 0x0F0F0F0Fu;
-      dhi = (wd >> 4) & 0x0F0F0F0Fu;
-    } else if (m == 1) {
-      dv[0] = fmaf(ubyte_f32<0>(dlo), st, nzs);
-      dv[1] = fmaf(ubyte_f32<0>(dhi), st, nzs);
-    } else if (m == 2) {
-      dq[0] = pack2(dv[0], dv[1], KIND);
-      dv[2] = ubyte_f32<1>(dlo);
-      dv[3] = ubyte_f32<1>(dhi);
-    } else if (m == 3) {
-      dq[1] = pack2(fmaf(dv[2], st, nzs), fmaf(dv[3], st, nzs), KIND);
-    } else if (m == 4) {
-      dv[0] = fmaf(ubyte_f32<2>(dlo), st, nzs);
-      dv[1] = fmaf(ubyte_f32<2>(dhi), st, nzs);
-    } else if (m == 5) {
-      dq[2] = pack2(dv[0], dv[1], KIND);
-      dv[2] = ubyte_f32<3>(dlo);
-      dv[3] = ubyte_f32<3>(dhi);
-    } else if (m == 6) {
-      dq[3] = pack2(fmaf(dv[2], st, nzs), fmaf(dv[3], st, nzs), KIND);
-    } else {
-      *reinterpret_cast<uint4*>(stage + brow + ((c ^ swz(tid)) << 4)) = make_uint4(dq[0], dq[1], dq[2], dq[3]);
-    }
-  };
+  f32x16 acc[FM][FN];
+  RowWeights<KIND> weights(cr, sr, zr, c_off, s_off, z_off);
+  w4a16_tile_loop<KIND, FN>({ra, lda_bytes}, weights, d_in / 64, false, lds, acc);
 
   const int wm = wave >> 1, wn = wave & 1;
   const int fr = lane & 31, fh = lane >> 5;
-  const int ra_off = (wm * 128 + fr) * KB;
-  const int rb_off = BM * KB + (wn * 128 + fr) * KB;
-  int slot[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) slot[q] = ((2 * q + fh) ^ swz(fr)) << 4;
-  f32x16 acc[FM][FN];
-  auto frag = [&](const char* stage, int sl, int r) -> uint4 {
-    const int off = r < FM ? ra_off + r * 32 * KB : rb_off + (r - FM) * 32 * KB;
-    return *reinterpret_cast<const uint4*>(stage + off + sl);
-  };
-  // one sub-step: 16 MFMAs on `use` while the next sub-step's fragments are read (if `reads`); after
-  // MFMA i of the 16, aux(i): at most one load, one LDS write or half a chunk of dequantization
-  auto substep = [&](auto zc, const uint4 (&use)[NR], uint4 (&nxt)[NR], const char* src, int sl, bool reads,
-                     auto aux) {
-    constexpr bool ZC = decltype(zc)::value;
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      const int fm = g >> 1, fn = (g & 1) * 2;
-      mma32<KIND, ZC>(use[fm], use[FM + fn], acc[fm][fn]);
-      __builtin_amdgcn_sched_barrier(0);
-      aux(2 * g);
-      if (reads) nxt[g] = frag(src, sl, g);
-      __builtin_amdgcn_sched_barrier(0);
-      mma32<KIND, ZC>(use[fm], use[FM + fn + 1], acc[fm][fn + 1]);
-      __builtin_amdgcn_sched_barrier(0);
-      aux(2 * g + 1);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  const std::false_type acc_in{};
-  const std::true_type acc_zero{};
-  auto none = [](int) {};
-
-  // prologue: stage 0 (activations and weights) into buffer 0; stage 1's activations and the first
-  // half of its weights into buffer 1 (the second half is done by step 0's first two sub-steps); the
-  // codes of step 2 requested
-  char* const buf[2] = {lds, lds + kTileStage};
-  const uint32_t bufa[2] = {lds_base, lds_base + kTileStage};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) dma_a(bufa[0], j, 0);
-  load_codes(0, 0);
-  load_codes(1, 1);
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-  params(0, 0);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) dequant_chunk(buf[0], 0, c);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) dma_a(bufa[1], j, 1);
-  params(1, 1);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) dequant_chunk(buf[1], 1, c);
-  // (past the last step the last step's codes are loaded again and not used: the loads stay
-  // unconditional, so no register is carried around the loop by a branch and copied while in flight)
-  load_codes(0, min(2, k_steps - 1));
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-  __syncthreads();
-  uint4 f0[NR], f1[NR];
-#pragma unroll
-  for (int r = 0; r < NR; ++r) f0[r] = frag(buf[0], slot[0], r);
-  substep(acc_zero, f0, f1, buf[0], slot[1], true, none);
-
-  // step kt: B C | barrier | D A'. The weights of step kt+1 are finished (chunks 4..7) in B and C,
-  // into its stage (read only after the barrier); D loads the activations of step kt+2 into the stage
-  // of step kt (freed by the barrier), and D and A' dequantize chunks 0..3 of step kt+2's weights into
-  // it; A' requests the codes of step kt+3 (into the register set B and C have just finished with).
-  // Codes are thus requested before the barrier that precedes their first use, whose wait covers
-  // them: the load counter completes in issue order, so a wait for codes requested after an
-  // activation DMA would also wait for that DMA, long before its barrier needs it.
-  // The parity of kt (buffer and codes register set) is a template argument: register arrays indexed
-  // at run time would be placed in scratch memory.
-  auto step = [&](int kt, auto parity) {
-    constexpr int P = decltype(parity)::value;
-    char* cur = buf[P];
-    char* nxt = buf[P ^ 1];
-    const bool pre2 = kt + 2 < k_steps;
-    // a part of a chunk after every MFMA: B chunks 4, 5 and C chunks 6, 7 of step kt+1
-    substep(acc_in, f1, f0, cur, slot[2], true, [&](int i) { dequant_part(nxt, P ^ 1, 4 + (i >> 3), i & 7); });
-    substep(acc_in, f0, f1, cur, slot[3], true, [&](int i) { dequant_part(nxt, P ^ 1, 6 + (i >> 3), i & 7); });
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    __syncthreads();
-    // D: step kt+2's activations into the freed stage (a load per pair of MFMAs) and its weight
-    // chunks 0, 1; A': the codes of step kt+3 and chunks 2, 3
-    substep(acc_in, f1, f0, nxt, slot[0], true, [&](int i) {
-      if (pre2 && (i & 1) == 0) dma_a(bufa[P], i >> 1, kt + 2);
-      if (pre2 && i == 0) params(P, kt + 2);
-      if (pre2) dequant_part(cur, P, i >> 3, i & 7);
-    });
-    substep(acc_in, f0, f1, nxt, slot[1], true, [&](int i) {
-      if (i == 0) load_codes(P ^ 1, min(kt + 3, k_steps - 1));
-      if (pre2) dequant_part(cur, P, 2 + (i >> 3), i & 7);
-    });
-  };
-  const std::integral_constant<int, 0> even{};
-  const std::integral_constant<int, 1> odd{};
-  // k_steps = d_in / 64 is even: steps 0 .. k_steps - 2 in pairs and one, then the last (odd) one
-  int kt = 0;
-  for (; kt + 2 < k_steps - 1; kt += 2) {
-    step(kt, even);
-    step(kt + 1, odd);
-  }
-  step(kt, even);
-  {  // the last step (k_steps - 1, odd): B C D
-    const char* cur = buf[1];
-    substep(acc_in, f1, f0, cur, slot[2], true, none);
-    substep(acc_in, f0, f1, cur, slot[3], true, none);
-    substep(acc_in, f1, f0, cur, slot[0], false, none);
-  }
-
   // element e of accumulator (i, j) in lane l: token 32 i + 8 (e / 4) + 4 (l / 32) + e % 4 of the
   // wave's 128, output row 32 j + l % 32 of its 128
   const int64_t t_w = m0 + wm * 128, f_w = n0 + wn * 128;

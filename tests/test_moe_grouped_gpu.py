@@ -55,7 +55,7 @@ def _plain_bound(x, W, off, K, backward, want, hs):
 # rows that are few for an expert, some tens, hundreds and thousands; ragged outputs, groups and rows
 SHAPES = [(1, 1, 128, 1), (1, 8, 256, 40), (2, 8, 4096, 64), (7, 3, 384, 300), (16, 1, 640, 33), (40, 60, 128, 272),
           (64, 4, 1152, 48), (100, 5, 256, 520), (300, 2, 384, 260), (513, 7, 128, 130), (1030, 3, 256, 264),
-          (2100, 2, 640, 520), (4200, 12, 128, 96)]
+          (2100, 2, 640, 520), (4200, 12, 128, 96), (700, 2, 256, 64), (650, 2, 256, 40), (700, 1, 384, 192), (2100, 3, 128, 128)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
