@@ -90,8 +90,7 @@ AWQ_API size_t awq_block_norm_backward_workspace_bytes(int64_t n_tokens, int64_t
  *   d_gate         float32 [d] when ld_gate == 0, else [n_tokens, ld_d_gate] of dtype.
  * Every output may be NULL (not wanted), but one at least is given. The sums over tokens are formed in a
  * fixed order.
- *   workspace      >= awq_block_norm_backward_workspace_bytes(n_tokens, d) bytes, 256-byte aligned; not
- *                  needed when no [d] gradient is wanted. */
+ *   workspace      >= awq_block_norm_backward_workspace_bytes(n_tokens, d) bytes, 256-byte aligned. */
 AWQ_API int awq_block_norm_backward(const void* y, int64_t ld_y, const void* residual, int64_t ld_residual, int dtype,
                                     int64_t n_tokens, int64_t d, const void* w_post, const void* gate,
                                     int64_t ld_gate, float res_scale, const void* w_pre, float eps,

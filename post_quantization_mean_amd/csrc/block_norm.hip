@@ -2,10 +2,11 @@
 // gradients:
 //   z = y / sqrt(mean(y^2) + eps) * w_post,  r' = residual + res_scale * gate * z,
 //   h = r' / sqrt(mean(r'^2) + eps) * w_pre.
-// Both directions are bound by memory: a row is read once into registers, its sums are formed across the
-// block, and each output is written once. One block handles a row (forward) or rows in a fixed stride
-// (backward, whose [d] gradients gather in registers over the block's rows, then over blocks in a second
-// kernel, in a fixed order: no atomics).
+// Both directions are bound by memory: a row is read once into registers (16 bytes per lane, kept packed),
+// its sums are formed across the block, and each output is written once. A block takes rows in a fixed
+// stride: the [d] weights stay in its registers, and the next row is loaded while the current one is
+// summed, so that loads stay in flight across the sums' barriers. The gradients of the [d] weights gather in
+// registers over the block's rows, then over blocks in a second kernel, in a fixed order: no atomics.
 #include <type_traits>
 
 #include "awq_moe.h"
@@ -15,214 +16,462 @@
 namespace awq {
 namespace {
 
-constexpr int64_t kMaxBlocks = 1 << 20;
-
 // mean of squares -> 1 / sqrt(. + eps)
 __device__ __forceinline__ float rstd_of(float sum, int d, float eps) {
   return 1.0f / sqrtf(sum / (float)d + eps);
 }
 
-template <typename T, int THREADS, int ITEMS>
-__global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormArgs a, Mat res_out, Mat h) {
-  constexpr int V = kVec<T>;
-  __shared__ float red[2][THREADS / 64];
-  const int d = a.d;
-  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    __syncthreads();  // the previous row's sums have been read
-    const T* yp = a.y.p ? (const T*)a.y.p + row * a.y.ld : nullptr;
-    const T* rp = (const T*)a.residual.p + row * a.residual.ld;
-    const T* gp = a.gate ? (const T*)a.gate + row * a.ld_gate : nullptr;
+// This thread's chunks of a row, packed.
+template <typename T, int ITEMS>
+struct Raw {
+  uint4 u[ITEMS];
+  __device__ __forceinline__ void load(const void* base, int64_t offset, const Place<T> (&p)[ITEMS]) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) u[i] = load_raw((const T*)base + offset, p[i]);
+  }
+  __device__ __forceinline__ void own(const Place<T> (&p)[ITEMS]) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) u[i] = own_raw<T>(u[i], p[i].skip);
+  }
+  __device__ __forceinline__ void fill(const uint4& v) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) u[i] = v;
+  }
+  __device__ __forceinline__ float at(int i, int k) const { return raw_f32<T>(u[i], k); }
+  // Keeps the chunks packed past this point: without it the compiler unpacks once and holds the float32
+  // values of weights across the loop and of the row across its sums, twice the registers.
+  __device__ __forceinline__ void keep_packed() {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) asm volatile("" : "+v"(u[i].x), "+v"(u[i].y), "+v"(u[i].z), "+v"(u[i].w));
+  }
+};
 
-    float r[ITEMS][V];
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) load_chunk(rp, (i * THREADS + (int)threadIdx.x) * V, d, r[i]);
-    if (yp) {
-      float y[ITEMS][V];
-      float s[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        load_chunk(yp, (i * THREADS + (int)threadIdx.x) * V, d, y[i]);
-#pragma unroll
-        for (int k = 0; k < V; ++k) s[0] = fmaf(y[i][k], y[i][k], s[0]);
-      }
-      float rs = 1.f;
-      if (a.w_post) {
-        block_sum<THREADS, 1>(s, red[0]);
-        rs = rstd_of(s[0], d, a.eps);
-      }
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        const int at = (i * THREADS + (int)threadIdx.x) * V;
-        float w[V];
-        if (a.w_post) {
-          load_chunk((const T*)a.w_post, at, d, w);
-#pragma unroll
-          for (int k = 0; k < V; ++k) y[i][k] = y[i][k] * rs * w[k];
-        }
-        if (gp) {
-          load_chunk(gp, at, d, w);
-#pragma unroll
-          for (int k = 0; k < V; ++k) y[i][k] *= w[k];
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) r[i][k] = fmaf(a.res_scale, y[i][k], r[i][k]);
-        if (res_out.p) store_chunk((T*)res_out.p + row * res_out.ld, at, d, r[i]);
-      }
+template <int... I>
+struct Seq {};
+template <int N, int... I>
+struct MakeSeq : MakeSeq<N - 1, N - 1, I...> {};
+template <int... I>
+struct MakeSeq<0, I...> {
+  typedef Seq<I...> type;
+};
+
+// The places of a thread's chunks: chunk i starts at element (i * threads + thread) * kVec.
+template <typename T, int ITEMS>
+struct Places {
+  Place<T> p[ITEMS];
+  template <int... I>
+  __device__ __forceinline__ Places(int d, Seq<I...>)
+      : p{Place<T>((I * (int)blockDim.x + (int)threadIdx.x) * kVec<T>, d)...} {}
+  __device__ __forceinline__ explicit Places(int d) : Places(d, typename MakeSeq<ITEMS>::type()) {}
+};
+
+// KEEP: the weights stay in registers and the next row is loaded ahead; otherwise (wide rows) neither, which
+// the registers would not hold.
+template <typename T, int ITEMS, int TMAX, bool KEEP>
+__global__ __launch_bounds__(TMAX) void block_norm_kernel(BlockNormArgs a, Mat res_out, Mat h) {
+  constexpr int V = kVec<T>;
+  __shared__ float red[2][16];
+  const int d = a.d;
+  const bool block = a.y.p != nullptr, token_gate = a.ld_gate != 0;
+  const bool ragged = d % (ITEMS * (int)blockDim.x * V) != 0;  // some lanes have less than whole chunks
+  const Places<T, ITEMS> at(d);
+  Raw<T, ITEMS> w1, w2, gt, y, r, yn, rn, gn;
+  w1.fill(raw_ones<T>());
+  gt.fill(raw_ones<T>());
+  y.fill(make_uint4(0, 0, 0, 0));
+  int64_t row = blockIdx.x;
+  auto load_row = [&](int64_t n, Raw<T, ITEMS>& ly, Raw<T, ITEMS>& lr, Raw<T, ITEMS>& lg) {
+    if (block) ly.load(a.y.p, n * a.y.ld, at.p);
+    lr.load(a.residual.p, n * a.residual.ld, at.p);
+    if (token_gate) lg.load(a.gate, n * a.ld_gate, at.p);
+  };
+  load_row(row, y, r, gt);
+  if (KEEP) {
+    if (a.w_post) w1.load(a.w_post, 0, at.p);
+    if (a.gate && !token_gate) gt.load(a.gate, 0, at.p);
+    if (a.w_pre) w2.load(a.w_pre, 0, at.p);
+  }
+  for (; row < a.n; row += gridDim.x) {
+    const int64_t next = row + gridDim.x;
+    if (KEEP && next < a.n) load_row(next, yn, rn, gn);
+    if (ragged) {
+      y.own(at.p);
+      r.own(at.p);
     }
-    if (h.p) {
+    if (KEEP) {
+      w1.keep_packed();
+      w2.keep_packed();
+      gt.keep_packed();
+    }
+    float rs = a.res_scale;
+    if (a.w_post) {
       float s[1] = {0.f};
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-        for (int k = 0; k < V; ++k) s[0] = fmaf(r[i][k], r[i][k], s[0]);
-      block_sum<THREADS, 1>(s, red[1]);
-      const float rs = rstd_of(s[0], d, a.eps);
+        for (int k = 0; k < V; ++k) s[0] = fmaf(y.at(i, k), y.at(i, k), s[0]);
+      block_sum(s, red[0]);
+      rs *= rstd_of(s[0], d, a.eps);
+      y.keep_packed();
+    }
+    if (!KEEP) {
+      if (a.w_post) w1.load(a.w_post, 0, at.p);
+      if (a.gate && !token_gate) gt.load(a.gate, 0, at.p);
+    }
+    float v[ITEMS][V], s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        v[i][k] = fmaf(y.at(i, k) * rs * w1.at(i, k), gt.at(i, k), r.at(i, k));
+        s[0] = fmaf(v[i][k], v[i][k], s[0]);
+      }
+      if (res_out.p) store_own((T*)res_out.p + row * res_out.ld, at.p[i], v[i]);
+    }
+    if (h.p) {
+      block_sum(s, red[1]);
+      const float rs2 = rstd_of(s[0], d, a.eps);
+      if (!KEEP) w2.load(a.w_pre, 0, at.p);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
-        const int at = (i * THREADS + (int)threadIdx.x) * V;
-        float w[V];
-        load_chunk((const T*)a.w_pre, at, d, w);
 #pragma unroll
-        for (int k = 0; k < V; ++k) w[k] *= r[i][k] * rs;
-        store_chunk((T*)h.p + row * h.ld, at, d, w);
+        for (int k = 0; k < V; ++k) v[i][k] *= rs2 * w2.at(i, k);
+        store_own((T*)h.p + row * h.ld, at.p[i], v[i]);
       }
     }
+    if (!(a.w_post && h.p)) __syncthreads();  // one sum a row: the next one reuses its floats
+    if (KEEP) {
+      y = yn;
+      r = rn;
+      if (token_gate) gt = gn;
+    } else
+    if (next < a.n) {
+      load_row(next, y, r, gt);
+    }
+  }
+}
+
+// Rows narrower than a chunk: one thread each.
+template <typename T>
+__global__ __launch_bounds__(256) void block_norm_narrow_kernel(BlockNormArgs a, Mat res_out, Mat h) {
+  constexpr int V = kVec<T>;
+  const int d = a.d;
+  for (int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; row < a.n; row += (int64_t)gridDim.x * blockDim.x) {
+    float y[V], v[V], s = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      y[c] = a.y.p && c < d ? to_f32(((const T*)a.y.p)[row * a.y.ld + c]) : 0.f;
+      s = fmaf(y[c], y[c], s);
+    }
+    const float rs = a.w_post ? a.res_scale * rstd_of(s, d, a.eps) : a.res_scale;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      if (c >= d) break;
+      const float w1 = a.w_post ? to_f32(((const T*)a.w_post)[c]) : 1.f;
+      const float gt = a.gate ? to_f32(((const T*)a.gate)[row * a.ld_gate + c]) : 1.f;
+      v[c] = fmaf(y[c] * rs * w1, gt, to_f32(((const T*)a.residual.p)[row * a.residual.ld + c]));
+      s2 = fmaf(v[c], v[c], s2);
+      if (res_out.p) ((T*)res_out.p)[row * res_out.ld + c] = from_f32<T>(v[c]);
+    }
+    const float rs2 = rstd_of(s2, d, a.eps);
+#pragma unroll
+    for (int c = 0; c < V; ++c)
+      if (h.p && c < d) ((T*)h.p)[row * h.ld + c] = from_f32<T>(v[c] * rs2 * to_f32(((const T*)a.w_pre)[c]));
   }
 }
 
 struct BlockNormGrads {
   CMat d_res, d_h;
-  Mat d_y, d_residual;
-  void* d_gate;  // with a gate per token
-  int64_t ld_d_gate;
-  float* partial;  // [3][blocks][d]: d_w_post, d_w_pre, d_gate; or NULL
-  bool sum_gate;
+  Mat d_y, d_residual, d_gate;  // d_gate: with a gate per token
+  float* partial;               // [3][blocks][d]: d_w_post, d_w_pre, d_gate; or NULL
 };
 
-template <typename T, int THREADS, int ITEMS>
-__global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormArgs a, BlockNormGrads g) {
-  constexpr int V = kVec<T>, W = THREADS / 64;
-  __shared__ float red[W * 4];
+template <typename T, int ITEMS, bool TOKEN>
+__global__ __launch_bounds__(512) void block_norm_backward_kernel(BlockNormArgs a, BlockNormGrads g) {
+  constexpr int V = kVec<T>;
+  __shared__ float red[4][16];
   const int d = a.d;
   const float inv_d = 1.0f / (float)d;
+  const bool block = a.y.p != nullptr;
+  const bool ragged = d % (ITEMS * (int)blockDim.x * V) != 0;
+  const Places<T, ITEMS> at(d);
+  struct {
+    Raw<T, ITEMS> y, r, dr, dh, gt;  // gt: with a gate per token
+  } c;
+  constexpr bool AHEAD = ITEMS <= 3;  // four chunks' registers do not hold the next row too
+  auto ahead = c;
+  auto load_into = [&](int64_t n, decltype(c)& c, Raw<T, ITEMS>& y) {
+    if (block) y.load(a.y.p, n * a.y.ld, at.p);
+    c.r.load(a.residual.p, n * a.residual.ld, at.p);
+    if (g.d_res.p) c.dr.load(g.d_res.p, n * g.d_res.ld, at.p);
+    if (g.d_h.p) c.dh.load(g.d_h.p, n * g.d_h.ld, at.p);
+    if (TOKEN) c.gt.load(a.gate, n * a.ld_gate, at.p);
+  };
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  c.y.fill(zero);
+  c.dr.fill(zero);
+  c.dh.fill(zero);
+  ahead = c;
+  Raw<T, ITEMS> w1, w2, wg;
+  wg.fill(raw_ones<T>());
+  w1.fill(raw_ones<T>());
+  w2.fill(raw_ones<T>());
   float sw1[ITEMS][V], sw2[ITEMS][V], sg[ITEMS][V];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
     for (int k = 0; k < V; ++k) sw1[i][k] = sw2[i][k] = sg[i][k] = 0.f;
 
-  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    const T* gp = a.gate ? (const T*)a.gate + row * a.ld_gate : nullptr;
-    float y[ITEMS][V], r[ITEMS][V], D[ITEMS][V], dhw[ITEMS][V];
-    float s1[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int at = (i * THREADS + (int)threadIdx.x) * V;
-      load_chunk((const T*)a.residual.p + row * a.residual.ld, at, d, r[i]);
-      if (a.y.p) load_chunk((const T*)a.y.p + row * a.y.ld, at, d, y[i]);
-      else
-#pragma unroll
-        for (int k = 0; k < V; ++k) y[i][k] = 0.f;
-      if (g.d_res.p) load_chunk((const T*)g.d_res.p + row * g.d_res.ld, at, d, D[i]);
-      else
-#pragma unroll
-        for (int k = 0; k < V; ++k) D[i][k] = 0.f;
-      if (g.d_h.p) load_chunk((const T*)g.d_h.p + row * g.d_h.ld, at, d, dhw[i]);
-      else
-#pragma unroll
-        for (int k = 0; k < V; ++k) dhw[i][k] = 0.f;
-#pragma unroll
-      for (int k = 0; k < V; ++k) s1[0] = fmaf(y[i][k], y[i][k], s1[0]);
+  int64_t row = blockIdx.x;
+  load_into(row, c, c.y);
+  if (a.w_post) w1.load(a.w_post, 0, at.p);
+  if (a.w_pre) w2.load(a.w_pre, 0, at.p);
+  if (!TOKEN && a.gate) wg.load(a.gate, 0, at.p);
+  for (; row < a.n; row += gridDim.x) {
+    const int64_t next = row + gridDim.x;
+    if (AHEAD && next < a.n) load_into(next, ahead, ahead.y);
+    if (ragged) {
+      c.y.own(at.p);
+      c.r.own(at.p);
+      c.dr.own(at.p);
+      c.dh.own(at.p);
     }
+    auto keep_packed = [&]() {
+      w1.keep_packed();
+      w2.keep_packed();
+      if (TOKEN) c.gt.keep_packed();
+      else wg.keep_packed();
+      c.y.keep_packed();
+      c.r.keep_packed();
+      c.dh.keep_packed();
+    };
+    keep_packed();
     float rs1 = 1.f;
-    __syncthreads();  // the previous row's last sums have been read
     if (a.w_post) {
-      block_sum<THREADS, 1>(s1, red);
-      rs1 = rstd_of(s1[0], d, a.eps);
-    }
-    // u1 in y; r' in r; d_h w_pre stays in dhw
-    float s2[2] = {0.f, 0.f};
+      float s[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int at = (i * THREADS + (int)threadIdx.x) * V;
-      float w1[V], gt[V], w2[V];
-      if (a.w_post) load_chunk((const T*)a.w_post, at, d, w1);
-      if (gp) load_chunk(gp, at, d, gt);
-      if (a.w_pre) load_chunk((const T*)a.w_pre, at, d, w2);
+      for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        y[i][k] *= rs1;
-        float z = a.w_post ? y[i][k] * w1[k] : y[i][k];
-        if (gp) z *= gt[k];
-        r[i][k] = fmaf(a.res_scale, z, r[i][k]);
-        s2[0] = fmaf(r[i][k], r[i][k], s2[0]);
-        if (a.w_pre) s2[1] = fmaf(dhw[i][k] * w2[k], r[i][k], s2[1]);
-      }
+        for (int k = 0; k < V; ++k) s[0] = fmaf(c.y.at(i, k), c.y.at(i, k), s[0]);
+      block_sum(s, red[0]);
+      rs1 = rstd_of(s[0], d, a.eps);
+      keep_packed();
     }
+    // r' from the packed inputs, as often as it is needed
+    const float ars = a.res_scale * rs1;
+    auto gate = [&](int i, int k) { return TOKEN ? c.gt.at(i, k) : wg.at(i, k); };
+    auto r_new = [&](int i, int k) { return fmaf(c.y.at(i, k) * ars * w1.at(i, k), gate(i, k), c.r.at(i, k)); };
     float rs2 = 0.f, m2 = 0.f;
     if (a.w_pre) {
-      block_sum<THREADS, 2>(s2, red + W);
-      rs2 = rstd_of(s2[0], d, a.eps);
-      m2 = s2[1] * rs2 * inv_d;  // mean(d_h w_pre u2)
+      float s[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float r = r_new(i, k);
+          s[0] = fmaf(r, r, s[0]);
+          s[1] = fmaf(c.dh.at(i, k) * w2.at(i, k), r, s[1]);
+        }
+      block_sum(s, red[1]);
+      rs2 = rstd_of(s[0], d, a.eps);
+      m2 = s[1] * rs2 * inv_d;  // mean(d_h w_pre u2)
+      keep_packed();
     }
-    float s3[1] = {0.f};
+    float t[ITEMS][V], s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int at = (i * THREADS + (int)threadIdx.x) * V;
-      float w1[V], gt[V], w2[V], dg[V];
-      if (a.w_post) load_chunk((const T*)a.w_post, at, d, w1);
-      if (gp) load_chunk(gp, at, d, gt);
-      if (a.w_pre) load_chunk((const T*)a.w_pre, at, d, w2);
+      float D[V], dg[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        if (a.w_pre) {
-          const float u2 = r[i][k] * rs2;
-          sw2[i][k] = fmaf(dhw[i][k], u2, sw2[i][k]);
-          D[i][k] = fmaf(rs2, dhw[i][k] * w2[k] - u2 * m2, D[i][k]);
-        }
-        r[i][k] = D[i][k];
-        const float ad = a.res_scale * D[i][k];
-        const float z = a.w_post ? y[i][k] * w1[k] : y[i][k];
-        dg[k] = ad * z;
-        sg[i][k] += dg[k];
-        const float t = gp ? ad * gt[k] : ad;
-        sw1[i][k] = fmaf(t, y[i][k], sw1[i][k]);
-        D[i][k] = a.w_post ? t * w1[k] : t;
-        s3[0] = fmaf(D[i][k], y[i][k], s3[0]);
+        const float u1 = c.y.at(i, k) * rs1, u2 = r_new(i, k) * rs2, dh = c.dh.at(i, k);
+        sw2[i][k] = fmaf(dh, u2, sw2[i][k]);
+        D[k] = fmaf(rs2, dh * w2.at(i, k) - u2 * m2, c.dr.at(i, k));
+        const float ad = a.res_scale * D[k];
+        dg[k] = ad * u1 * w1.at(i, k);
+        if (!TOKEN) sg[i][k] += dg[k];
+        const float dz = ad * gate(i, k);
+        sw1[i][k] = fmaf(dz, u1, sw1[i][k]);
+        t[i][k] = dz * w1.at(i, k);
+        s[0] = fmaf(t[i][k], u1, s[0]);
       }
-      if (g.d_residual.p) store_chunk((T*)g.d_residual.p + row * g.d_residual.ld, at, d, r[i]);
-      if (g.d_gate && !g.sum_gate) store_chunk((T*)g.d_gate + row * g.ld_d_gate, at, d, dg);
+      if (g.d_residual.p) store_own((T*)g.d_residual.p + row * g.d_residual.ld, at.p[i], D);
+      if (TOKEN && g.d_gate.p) store_own((T*)g.d_gate.p + row * g.d_gate.ld, at.p[i], dg);
     }
+    // the next row's loads: only y of this row is still needed
     if (g.d_y.p) {
       float m1 = 0.f;
       if (a.w_post) {
-        block_sum<THREADS, 1>(s3, red + 3 * W);
-        m1 = s3[0] * inv_d;
+        block_sum(s, red[3]);
+        m1 = s[0] * inv_d * rs1;  // mean(t u1) / sqrt(.), times y below
+        c.y.keep_packed();
       }
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
-        const int at = (i * THREADS + (int)threadIdx.x) * V;
-        float o[V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = a.w_post ? rs1 * (D[i][k] - y[i][k] * m1) : D[i][k];
-        store_chunk((T*)g.d_y.p + row * g.d_y.ld, at, d, o);
+        for (int k = 0; k < V; ++k) t[i][k] = rs1 * (t[i][k] - c.y.at(i, k) * m1);
+        store_own((T*)g.d_y.p + row * g.d_y.ld, at.p[i], t[i]);
       }
     }
+    __syncthreads();  // the next row's sums reuse the floats of this one's
+    if (AHEAD) c = ahead;
+    else if (next < a.n) load_into(next, c, c.y);
   }
   if (g.partial) {
     const int64_t plane = (int64_t)gridDim.x * d;
     float* p = g.partial + (int64_t)blockIdx.x * d;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int at = (i * THREADS + (int)threadIdx.x) * V;
+    for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (at + k < d) {
-          p[at + k] = sw1[i][k];
-          p[plane + at + k] = sw2[i][k];
-          p[2 * plane + at + k] = sg[i][k];
+      for (int k = 0; k < V; ++k) {
+        const int e = at.p[i].at + k;
+        if (k >= at.p[i].skip) {
+          p[e] = sw1[i][k];
+          p[plane + e] = sw2[i][k];
+          p[2 * plane + e] = sg[i][k];
         }
+      }
+  }
+}
+
+// Rows too wide for the registers of a block, or narrower than a chunk, take two kernels: the first finds each
+// row's norms and means (reading the row again in every pass, from the caches), with which the second is
+// element-wise: its blocks walk down strips of columns, write the rows' gradients and keep the sums over tokens
+// in registers. 10 instead of 6 passes over the data.
+struct RowStats {
+  float rs1, rs2, m2, m1;  // m1: mean(t u1) rs1, times y in d_y
+};
+
+// A chunk of every input at columns c .. c + kVec - 1 of a row, and what both kernels form of it.
+template <typename T>
+struct WideChunk {
+  static constexpr int V = kVec<T>;
+  float y[V], r[V], dr[V], dh[V], w1[V], w2[V], gt[V];
+  static __device__ __forceinline__ void get(const void* p, int64_t offset, int c, int d, float none, float (&v)[V]) {
+    if (p) {
+      load_chunk((const T*)p + offset, c, d, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] = none;
     }
+  }
+  __device__ __forceinline__ void load_row(const BlockNormArgs& a, const BlockNormGrads& g, int64_t row, int c) {
+    get(a.y.p, row * a.y.ld, c, a.d, 0.f, y);
+    get(a.residual.p, row * a.residual.ld, c, a.d, 0.f, r);
+    get(g.d_res.p, row * g.d_res.ld, c, a.d, 0.f, dr);
+    get(g.d_h.p, row * g.d_h.ld, c, a.d, 0.f, dh);
+    if (a.ld_gate != 0) get(a.gate, row * a.ld_gate, c, a.d, 1.f, gt);
+  }
+  __device__ __forceinline__ void load_weights(const BlockNormArgs& a, int c) {
+    get(a.w_post, 0, c, a.d, 1.f, w1);
+    get(a.w_pre, 0, c, a.d, 1.f, w2);
+    if (a.ld_gate == 0) get(a.gate, 0, c, a.d, 1.f, gt);
+  }
+  __device__ __forceinline__ float r_new(int k, float ars) const { return fmaf(y[k] * ars * w1[k], gt[k], r[k]); }
+  __device__ __forceinline__ float grad(int k, const RowStats& s, float u2) const {
+    return fmaf(s.rs2, dh[k] * w2[k] - u2 * s.m2, dr[k]);
+  }
+};
+
+template <typename T>
+__global__ __launch_bounds__(512) void block_norm_stats_kernel(BlockNormArgs a, BlockNormGrads g, RowStats* stats) {
+  constexpr int V = kVec<T>;
+  __shared__ float red[4][16];
+  const int d = a.d, first = (int)threadIdx.x * V, step = (int)blockDim.x * V;
+  const float inv_d = 1.0f / (float)d;
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    RowStats st = {1.f, 0.f, 0.f, 0.f};
+    __syncthreads();  // the previous row's sums have been read
+    if (a.w_post) {
+      float s[1] = {0.f};
+#pragma unroll 4
+      for (int c = first; c < d; c += step) {
+        float y[V];
+        load_chunk((const T*)a.y.p + row * a.y.ld, c, d, y);
+#pragma unroll
+        for (int k = 0; k < V; ++k) s[0] = fmaf(y[k], y[k], s[0]);
+      }
+      block_sum(s, red[0]);
+      st.rs1 = rstd_of(s[0], d, a.eps);
+    }
+    const float ars = a.res_scale * st.rs1;
+    if (a.w_pre) {
+      float s[2] = {0.f, 0.f};
+#pragma unroll 2
+      for (int c = first; c < d; c += step) {
+        WideChunk<T> x;
+        x.load_row(a, g, row, c);
+        x.load_weights(a, c);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float r = x.r_new(k, ars);
+          s[0] = fmaf(r, r, s[0]);
+          s[1] = fmaf(x.dh[k] * x.w2[k], r, s[1]);
+        }
+      }
+      block_sum(s, red[1]);
+      st.rs2 = rstd_of(s[0], d, a.eps);
+      st.m2 = s[1] * st.rs2 * inv_d;
+    }
+    if (a.w_post) {
+      float s[1] = {0.f};
+#pragma unroll 2
+      for (int c = first; c < d; c += step) {
+        WideChunk<T> x;
+        x.load_row(a, g, row, c);
+        x.load_weights(a, c);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          s[0] = fmaf(a.res_scale * x.grad(k, st, x.r_new(k, ars) * st.rs2) * x.gt[k] * x.w1[k], x.y[k] * st.rs1, s[0]);
+      }
+      block_sum(s, red[3]);
+      st.m1 = s[0] * inv_d * st.rs1;
+    }
+    if (threadIdx.x == 0) stats[row] = st;
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void block_norm_columns_kernel(BlockNormArgs a, BlockNormGrads g,
+                                                                 const RowStats* stats) {
+  constexpr int V = kVec<T>;
+  const int d = a.d, c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * V;
+  if (c >= d) return;
+  float sw1[V], sw2[V], sg[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) sw1[k] = sw2[k] = sg[k] = 0.f;
+  WideChunk<T> x;
+  x.load_weights(a, c);
+#pragma unroll 2
+  for (int64_t row = blockIdx.y; row < a.n; row += gridDim.y) {
+    x.load_row(a, g, row, c);
+    const RowStats st = stats[row];
+    const float ars = a.res_scale * st.rs1;
+    float D[V], dy[V], dg[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float u1 = x.y[k] * st.rs1, u2 = x.r_new(k, ars) * st.rs2;
+      D[k] = x.grad(k, st, u2);
+      const float ad = a.res_scale * D[k], dz = ad * x.gt[k];
+      dg[k] = ad * u1 * x.w1[k];
+      dy[k] = st.rs1 * (dz * x.w1[k] - x.y[k] * st.m1);
+      sw1[k] = fmaf(dz, u1, sw1[k]);
+      sw2[k] = fmaf(x.dh[k], u2, sw2[k]);
+      sg[k] += dg[k];
+    }
+    if (g.d_residual.p) store_chunk((T*)g.d_residual.p + row * g.d_residual.ld, c, d, D);
+    if (g.d_gate.p) store_chunk((T*)g.d_gate.p + row * g.d_gate.ld, c, d, dg);
+    if (g.d_y.p) store_chunk((T*)g.d_y.p + row * g.d_y.ld, c, d, dy);
+  }
+  if (g.partial) {
+    const int64_t plane = (int64_t)gridDim.y * d;
+    float* p = g.partial + (int64_t)blockIdx.y * d + c;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (c + k < d) {
+        p[k] = sw1[k];
+        p[plane + k] = sw2[k];
+        p[2 * plane + k] = sg[k];
+      }
   }
 }
 
@@ -238,8 +487,10 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, 
   if (!out) return;
   const float* p = partial + (int64_t)blockIdx.y * blocks * d;
   float s = 0.f;
-  if (c < d)
+  if (c < d) {
+#pragma unroll 8
     for (int b = run; b < blocks; b += 16) s += p[(int64_t)b * d + c];
+  }
   part[run][threadIdx.x & 63] = s;
   __syncthreads();
   if (run == 0 && c < d) {
@@ -248,54 +499,104 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, 
   }
 }
 
-template <typename T, typename F>
-hipError_t with_shape(int d, F f) {
-  const int chunks = (d + kVec<T> - 1) / kVec<T>;
-  using std::integral_constant;
-  if (chunks <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  else if (chunks <= 256) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  else if (chunks <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  else if (chunks <= 1024) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-  else if (chunks <= 2048) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-  else if (chunks <= 4096) f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
-  else f(integral_constant<int, 1024>{}, integral_constant<int, 8>{});
+template <typename F>
+hipError_t with_dtype(int dtype, F f) {
+  if (dtype == AWQ_DTYPE_BF16) f(Bf16{});
+  else if (dtype == AWQ_DTYPE_F16) f(F16{});
+  else f(0.f);
   return hipGetLastError();
 }
 
-template <typename F>
-hipError_t with_dtype(int dtype, F f) {
-  if (dtype == AWQ_DTYPE_BF16) return f(Bf16{});
-  if (dtype == AWQ_DTYPE_F16) return f(F16{});
-  return f(0.f);
+// The block for a row of d elements: as few threads as hold it with `items` chunks each.
+int row_threads(int d, int vec, int items) { return ((d + vec * items - 1) / (vec * items) + 63) / 64 * 64; }
+
+// Blocks that keep about `per_cu` threads on each compute unit.
+int64_t row_blocks(int64_t n, int threads, int per_cu) {
+  const int64_t b = (int64_t)256 * (per_cu / threads > 0 ? per_cu / threads : 1);
+  return n < b ? n : b;
 }
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 }  // namespace
 
 hipError_t launch_block_norm(const BlockNormArgs& a, int dtype, Mat res_out, Mat h, hipStream_t st) {
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return with_shape<T>(a.d, [&](auto threads, auto items) {
-      hipLaunchKernelGGL((block_norm_kernel<T, decltype(threads)::value, decltype(items)::value>),
-                         dim3((unsigned)(a.n < kMaxBlocks ? a.n : kMaxBlocks)), dim3(decltype(threads)::value), 0, st, a,
-                         res_out, h);
-    });
+    auto go = [&](auto items, auto keep) {
+      constexpr int I = decltype(items)::value;
+      const int threads = row_threads(a.d, kVec<T>, I);
+      hipLaunchKernelGGL((block_norm_kernel<T, I, 1024, decltype(keep)::value>),
+                         dim3((unsigned)row_blocks(a.n, threads, 1024)), dim3(threads), 0, st, a, res_out, h);
+    };
+    const int chunks = (a.d + kVec<T> - 1) / kVec<T>;
+    if (a.d < kVec<T>)
+      hipLaunchKernelGGL((block_norm_narrow_kernel<T>), dim3((unsigned)row_blocks((a.n + 255) / 256, 256, 2048)),
+                         dim3(256), 0, st, a, res_out, h);
+    else if (chunks <= 128) go(Int<1>{}, std::true_type{});
+    else if (chunks <= 2048) go(Int<2>{}, std::true_type{});
+    else if (chunks <= 4096) go(Int<4>{}, std::false_type{});
+    else if constexpr (sizeof(T) == 4) go(Int<8>{}, std::false_type{});
   });
 }
 
-int block_norm_backward_blocks(int64_t n_tokens, int64_t d) { return (int)(n_tokens < 512 ? n_tokens : 512); }
+// Rows whose gradient is held in registers; the others take the two kernels.
+constexpr int kBackwardWidth = 8192;
+bool wide_backward(int64_t d) { return d > kBackwardWidth || d < 8; }
+
+// Blocks of partial sums. In registers: two blocks on a compute unit, which is what these allow. Wide: strips
+// of at least 1024 columns (float32) by so many rows' strides that about 1024 blocks walk down the strips.
+int block_norm_backward_blocks(int64_t n_tokens, int64_t d) {
+  if (wide_backward(d)) {
+    const int64_t strips = (d + 1023) / 1024, b = (1024 + strips - 1) / strips;
+    return (int)(n_tokens < b ? n_tokens : b);
+  }
+  return (int)row_blocks(n_tokens, row_threads((int)d, 8, 1), 1024);
+}
+
+size_t block_norm_backward_partial_floats(int64_t n_tokens, int64_t d) {
+  return (size_t)3 * (size_t)block_norm_backward_blocks(n_tokens, d) * (size_t)d;
+}
+
+size_t block_norm_backward_stats_bytes(int64_t n_tokens, int64_t d) {
+  return wide_backward(d) ? (size_t)n_tokens * sizeof(RowStats) : 0;
+}
 
 hipError_t launch_block_norm_backward(const BlockNormArgs& a, int dtype, CMat d_res, CMat d_h, Mat d_y, Mat d_residual,
                                       float* d_w_post, float* d_w_pre, void* d_gate, int64_t ld_d_gate,
-                                      float* partial, hipStream_t st) {
-  const int blocks = block_norm_backward_blocks(a.n, a.d);
+                                      void* stats_space, float* partial_space, hipStream_t st) {
   const bool sum_gate = a.ld_gate == 0;
-  const BlockNormGrads g{d_res, d_h, d_y, d_residual, d_gate, ld_d_gate, partial, sum_gate};
+  float* const partial = d_w_post || d_w_pre || (d_gate && sum_gate) ? partial_space : nullptr;
+  int blocks = block_norm_backward_blocks(a.n, a.d);
+  const BlockNormGrads g{d_res, d_h, d_y, d_residual, {sum_gate ? nullptr : d_gate, ld_d_gate}, partial};
   hipError_t e = with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return with_shape<T>(a.d, [&](auto threads, auto items) {
-      hipLaunchKernelGGL((block_norm_backward_kernel<T, decltype(threads)::value, decltype(items)::value>),
-                         dim3((unsigned)blocks), dim3(decltype(threads)::value), 0, st, a, g);
-    });
+    constexpr int V = kVec<T>;
+    if (wide_backward(a.d)) {
+      RowStats* stats = static_cast<RowStats*>(stats_space);
+      const int threads = a.d < 64 * V ? 64 : 512;
+      hipLaunchKernelGGL((block_norm_stats_kernel<T>), dim3((unsigned)row_blocks(a.n, threads, 2048)), dim3(threads),
+                         0, st, a, g, stats);
+      hipLaunchKernelGGL((block_norm_columns_kernel<T>), dim3((unsigned)((a.d + 256 * V - 1) / (256 * V)), blocks),
+                         dim3(256), 0, st, a, g, stats);
+      return;
+    }
+    // float32 rows keep the memory busy with one block on a compute unit, and have half the partial sums to add
+    if (sizeof(T) == 4) blocks = (int)row_blocks(a.n, row_threads(a.d, 8, 1), 512);
+    auto go = [&](auto items) {
+      constexpr int I = decltype(items)::value;
+      const dim3 grid((unsigned)blocks), block(row_threads(a.d, V, I));
+      if (sum_gate) hipLaunchKernelGGL((block_norm_backward_kernel<T, I, false>), grid, block, 0, st, a, g);
+      else hipLaunchKernelGGL((block_norm_backward_kernel<T, I, true>), grid, block, 0, st, a, g);
+    };
+    const int chunks = (a.d + V - 1) / V;
+    if (chunks <= 64) go(Int<1>{});
+    else if (chunks <= 1024) go(Int<2>{});
+    else if constexpr (sizeof(T) == 4) {
+      if (chunks <= 1536) go(Int<3>{});
+      else go(Int<4>{});
+    }
   });
   if (e != hipSuccess || !partial) return e;
   const ColumnSums outs{{d_w_post, d_w_pre, sum_gate ? (float*)d_gate : nullptr}};

@@ -32,12 +32,12 @@ struct BlockNormArgs {
 
 hipError_t launch_block_norm(const BlockNormArgs& a, int dtype, Mat res_out, Mat h, hipStream_t stream);
 
-// Blocks (rows of partial sums) of the backward pass.
-int block_norm_backward_blocks(int64_t n_tokens, int64_t d);
-// partial: 3 x blocks x d float32, or NULL when none of the [d] gradients is wanted
+// The workspace of the backward pass: row statistics (wide rows), and partial sums over tokens.
+size_t block_norm_backward_stats_bytes(int64_t n_tokens, int64_t d);
+size_t block_norm_backward_partial_floats(int64_t n_tokens, int64_t d);
 hipError_t launch_block_norm_backward(const BlockNormArgs& a, int dtype, CMat d_res, CMat d_h, Mat d_y, Mat d_residual,
                                       float* d_w_post, float* d_w_pre, void* d_gate, int64_t ld_d_gate,
-                                      float* partial, hipStream_t stream);
+                                      void* stats_space, float* partial_space, hipStream_t stream);
 
 // Blocks of the sort; 1: a single launch without workspace.
 int moe_sort_blocks(int64_t n_slots);

@@ -185,7 +185,8 @@ int awq_block_norm(const void* y, int64_t ld_y, const void* residual, int64_t ld
 
 size_t awq_block_norm_backward_workspace_bytes(int64_t n_tokens, int64_t d) {
   if (!norm_sizes_ok(n_tokens, d)) return 0;
-  return round_up((size_t)3 * (size_t)awq::block_norm_backward_blocks(n_tokens, d) * (size_t)d * sizeof(float), 256);
+  return round_up(awq::block_norm_backward_stats_bytes(n_tokens, d), 256) +
+         round_up(awq::block_norm_backward_partial_floats(n_tokens, d) * sizeof(float), 256);
 }
 
 int awq_block_norm_backward(const void* y, int64_t ld_y, const void* residual, int64_t ld_residual, int dtype,
@@ -212,12 +213,11 @@ int awq_block_norm_backward(const void* y, int64_t ld_y, const void* residual, i
   const bool sum_gate = d_gate && ld_gate == 0;
   if (sum_gate) TRY(check_vec("d_gate", d_gate, 4));
   else if (d_gate) TRY(check_mat("d_gate", d_gate, ld_d_gate, d, dtype));
-  const bool sums = d_w_post || d_w_pre || sum_gate;
-  TRY(check_workspace(workspace, workspace_bytes,
-                      sums ? awq_block_norm_backward_workspace_bytes(n_tokens, d) : 0));
+  TRY(check_workspace(workspace, workspace_bytes, awq_block_norm_backward_workspace_bytes(n_tokens, d)));
+  const size_t stats = round_up(awq::block_norm_backward_stats_bytes(n_tokens, d), 256);
   hipError_t e = awq::launch_block_norm_backward(a, dtype, {d_res_out, ld_d_res_out}, {d_h, ld_d_h}, {d_y, ld_d_y},
                                                  {d_residual, ld_d_residual}, d_w_post, d_w_pre, d_gate, ld_d_gate,
-                                                 sums ? (float*)workspace : nullptr, (hipStream_t)stream);
+                                                 workspace, (float*)((char*)workspace + stats), (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "block_norm_backward launch");
   return ok();
 }

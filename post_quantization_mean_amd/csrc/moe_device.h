@@ -67,34 +67,98 @@ __device__ __forceinline__ void store_chunk(T* row, int i, int d, const float (&
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
+// A thread's chunk of a row of width d >= kVec as whole loads without a branch: the chunk at element i, moved back
+// to end with the row where it would pass its end. `skip` counts its leading elements that belong to the chunk
+// before (kVec or more: all of it).
+template <typename T>
+struct Place {
+  int at, skip;
+  __device__ __forceinline__ Place(int i, int d) : at(min(i, d - kVec<T>)), skip(i - min(i, d - kVec<T>)) {}
+};
+
+template <typename T>
+__device__ __forceinline__ uint4 load_raw(const T* row, const Place<T>& p) {
+  return __builtin_bit_cast(uint4, *reinterpret_cast<const Chunk<T>*>(row + p.at));
 }
 
-// Sums of N values over the block's THREADS threads, in every thread. `red` holds THREADS / 64 * N floats
-// used by this call alone between two barriers of other calls.
-template <int THREADS, int N>
+// The chunk with the skipped elements zero.
+template <typename T>
+__device__ __forceinline__ uint4 own_raw(uint4 u, int skip) {
+  constexpr int per = 4 / (int)sizeof(T);
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = skip - j * per;  // skipped elements of this word
+    w[j] = n <= 0 ? w[j] : n >= per ? 0u : w[j] & 0xFFFF0000u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_own(T* row, const Place<T>& p, const float (&v)[kVec<T>]) {
+  Chunk<T> c;
+#pragma unroll
+  for (int k = 0; k < kVec<T>; ++k) c.v[k] = from_f32<T>(v[k]);
+  if (p.skip == 0) {
+    *reinterpret_cast<Chunk<T>*>(row + p.at) = c;
+  } else {
+#pragma unroll
+    for (int k = 0; k < kVec<T>; ++k)
+      if (k >= p.skip) row[p.at + k] = c.v[k];
+  }
+}
+
+// Element k of a chunk's bits.
+template <typename T>
+__device__ __forceinline__ float raw_f32(const uint4& u, int k) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[k]);
+  else if constexpr (__is_same(T, Bf16)) return __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)(k & 1 ? w[k >> 1] >> 16 : w[k >> 1]));
+}
+
+// A chunk of ones.
+template <typename T>
+__device__ __forceinline__ uint4 raw_ones() {
+  const uint32_t one = sizeof(T) == 4 ? 0x3F800000u : __is_same(T, Bf16) ? 0x3F803F80u : 0x3C003C00u;
+  return make_uint4(one, one, one, one);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(
+                 float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+
+// Sum over each row of 16 lanes, in every lane.
+__device__ __forceinline__ float row16_sum(float v) {
+  return dpp_add<kDppRowMirror>(dpp_add<kDppHalfMirror>(dpp_add<kDppXor2>(dpp_add<kDppXor1>(v))));
+}
+
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+
+// Sums of N values over a block of up to 16 waves, in every thread, in a fixed order. `red` holds 16 N
+// floats used by this call alone between two barriers of other calls.
+template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* red) {
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
-  if constexpr (THREADS > 64) {
-    constexpr int W = THREADS / 64;
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
+  if (waves == 1) return;
+  if (lane == 0) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) red[wave * N + k] = v[k];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) s += red[w * N + k];
-      v[k] = s;
-    }
+    for (int k = 0; k < N; ++k) red[k * 16 + (threadIdx.x >> 6)] = v[k];
   }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = row16_sum((lane & 15) < waves ? red[k * 16 + (lane & 15)] : 0.f);
 }
 
 }  // namespace awq

@@ -191,13 +191,10 @@ def awq_block_norm_backward(y, residual: torch.Tensor, d_res_out, d_h, w_pre=Non
             o = out.get(name)
             o = torch.empty(d, dtype=torch.float32, device=dev) if o is None else o
             res[name], ptr[name] = o, (_vector(o, name, torch.float32, d, dev), 0)
-    pw, nb = None, 0
-    if ptr["d_w_pre"][0] or ptr["d_w_post"][0] or (ptr["d_gate"][0] and gate.dim() == 1):
-        nb = lib.awq_block_norm_backward_workspace_bytes(n, d)
-        workspace = _workspace(nb, dev, workspace)
-        pw, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    workspace = _workspace(lib.awq_block_norm_backward_workspace_bytes(n, d), dev, workspace)
     _call(lib.awq_block_norm_backward, dev, stream, *args, pr, ldr, ph, ldh, *ptr["d_y"], *ptr["d_residual"],
-          ptr["d_w_post"][0], ptr["d_w_pre"][0], *ptr["d_gate"], pw, nb)
+          ptr["d_w_post"][0], ptr["d_w_pre"][0], *ptr["d_gate"], workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return res
 
 
