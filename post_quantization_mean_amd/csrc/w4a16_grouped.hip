@@ -63,185 +63,6 @@ int64_t most_tiles(int64_t n_rows, int n_experts, int bm) {
   return used + (n_rows - used) / bm;
 }
 
-// act(g) * u in float32
-__device__ __forceinline__ float gated(float g, float u, int mode) {
-  const float a = mode == AWQ_GROUPED_GATED_SILU ? g / (1.0f + __expf(-g)) : (g <= 0.0f ? 0.0f : g);  // NaN stays
-  return a * u;
-}
-
-// ---------------------------------------------------------------- few rows per expert
-
-constexpr int kSmallWaves = 8;
-
-// 16 MT rows x 16 NT output rows per block; the eight waves take contiguous ranges of the groups and
-// their partial products are added in wave order. GATED: tile 0 is of the gate, tile 1 of the up matrix.
-template <int KIND, typename OutT, int NT, int MT, bool GATED>
-__global__ __launch_bounds__(64 * kSmallWaves) void grouped_small_kernel(GroupedArgs a) {
-  static_assert(!GATED || NT == 2, "a gate tile and an up tile");
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  RowTile t;
-  if (!find_tile(a.offsets, a.n_experts, a.n_rows, 16 * MT, blockIdx.y, t)) return;
-  const int n = lane & 15, kq = lane >> 4;
-  const int G = a.d_in / kGroup, GZ = (G + 1) / 2;
-  const int width = GATED ? a.d_out / 2 : a.d_out;  // of y
-  const int col0 = blockIdx.x * (GATED ? 16 : 16 * NT);
-  const int g_begin = (G * wave) / kSmallWaves, g_end = (G * (wave + 1)) / kSmallWaves;
-  const uint8_t* crow[NT];
-  const uint16_t* srow[NT];
-  const uint8_t* zrow[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int c = min(col0 + (GATED ? 0 : 16 * j) + n, width - 1);
-    const int64_t row = (int64_t)t.expert * a.d_out + (GATED ? j * width : 0) + c;
-    crow[j] = a.codes + row * (a.d_in / 2) + kq * 16;
-    srow[j] = a.steps + row * G;
-    zrow[j] = a.zeros + row * GZ;
-  }
-  const uint16_t* xrow[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-    xrow[m] = (const uint16_t*)a.x.p + (int64_t)(t.row0 + min(16 * m + n, t.rows - 1)) * a.x.ld + kq * 32;
-  f32x4 acc[MT][NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int g = g_begin; g < g_end; ++g) {
-    uint4 cw[NT];
-    float st[NT], nzs[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      cw[j] = *reinterpret_cast<const uint4*>(crow[j] + (int64_t)g * (kGroup / 2));
-      group_params(srow[j][g], zrow[j][g >> 1], g, st[j], nzs[j]);
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      uint4 x[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) x[m] = *reinterpret_cast<const uint4*>(xrow[m] + g * kGroup + s * 8);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const uint32_t w = s == 0 ? cw[j].x : s == 1 ? cw[j].y : s == 2 ? cw[j].z : cw[j].w;
-        const uint4 b = dequant8<KIND>(w, st[j], nzs[j]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m][j] = mma<KIND>(x[m], b, acc[m][j]);
-      }
-    }
-  }
-  __shared__ f32x4 red[kSmallWaves][MT * NT][64];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) red[wave][m * NT + j][lane] = acc[m][j];
-  __syncthreads();
-  constexpr int kSums = GATED ? MT : MT * NT;
-  if (wave < kSums) {
-    f32x4 s[GATED ? 2 : 1];
-#pragma unroll
-    for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-      const int at = GATED ? 2 * wave + q : wave;
-      s[q] = red[0][at][lane];
-#pragma unroll
-      for (int w = 1; w < kSmallWaves; ++w) s[q] += red[w][at][lane];
-    }
-    const int m = GATED ? wave : wave / NT, j = GATED ? 0 : wave % NT;
-    const int c = col0 + 16 * j + n;
-    OutT* y = (OutT*)a.y.p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 16 * m + 4 * kq + i;
-      float v = s[0][i];
-      if constexpr (GATED) v = gated(v, s[1][i], a.mode);
-      if (c < width && r < t.rows) y[(int64_t)(t.row0 + r) * a.y.ld + c] = to_out<OutT>(v, KIND);
-    }
-  }
-}
-
-// ---------------------------------------------------------------- the gradient with respect to the rows
-
-// 16 MT rows of d_x x one group's 128 columns per wave; the contraction runs over the output rows o. Lane
-// n = l mod 16 of lane group kq reads, for each of its eight k = 8 kq + e, the word of row o + k that holds
-// columns 8 n .. 8 n + 7, so that its eight column tiles j (column 8 n + j in column place n) each find
-// their eight consecutive k in the lane's own registers: the transposition costs no exchange.
-template <int KIND, typename OutT, int MT>
-__global__ __launch_bounds__(256) void grouped_backward_simple_kernel(GroupedArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  RowTile t;
-  if (!find_tile(a.offsets, a.n_experts, a.n_rows, 16 * MT, blockIdx.y, t)) return;
-  const int G = a.d_in / kGroup, GZ = (G + 1) / 2;
-  const int g = blockIdx.x * 4 + wave;
-  if (g >= G) return;
-  const int n = lane & 15, kq = lane >> 4;
-  const int64_t row_e = (int64_t)t.expert * a.d_out;
-  f32x4 acc[MT][8];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int o0 = 0; o0 < a.d_out; o0 += 32) {
-    uint32_t w[8];
-    float st[8], nzs[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int o = o0 + 8 * kq + e;
-      const int64_t row = row_e + min(o, a.d_out - 1);
-      w[e] = *reinterpret_cast<const uint32_t*>(a.codes + row * (a.d_in / 2) + g * (kGroup / 2) + 4 * n);
-      group_params(a.steps[row * G + g], a.zeros[row * GZ + (g >> 1)], g, st[e], nzs[e]);
-      if (o >= a.d_out) w[e] = 0, st[e] = nzs[e] = 0.f;
-    }
-    uint4 x[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const uint16_t* xr = (const uint16_t*)a.x.p + (int64_t)(t.row0 + min(16 * m + n, t.rows - 1)) * a.x.ld;
-      const int o = o0 + 8 * kq;
-      x[m] = make_uint4(0, 0, 0, 0);
-      if (o + 8 <= a.d_out) {
-        x[m] = *reinterpret_cast<const uint4*>(xr + o);
-      } else if (o < a.d_out) {
-        uint32_t q[4] = {0, 0, 0, 0};
-        for (int e = 0; o + e < a.d_out; ++e) q[e >> 1] |= (uint32_t)xr[o + e] << (16 * (e & 1));
-        x[m] = make_uint4(q[0], q[1], q[2], q[3]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = fmaf((float)((w[e] >> (4 * j)) & 15u), st[e], nzs[e]);
-      const uint4 b = make_uint4(pack2(v[0], v[1], KIND), pack2(v[2], v[3], KIND), pack2(v[4], v[5], KIND),
-                                 pack2(v[6], v[7], KIND));
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[m][j] = mma<KIND>(x[m], b, acc[m][j]);
-    }
-  }
-  OutT* y = (OutT*)a.y.p;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 16 * m + 4 * kq + i;
-      if (r >= t.rows) continue;
-      OutT* yr = y + (int64_t)(t.row0 + r) * a.y.ld + g * kGroup + 8 * n;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) yr[j] = to_out<OutT>(acc[m][j][i], KIND);
-    }
-}
-
-// ---------------------------------------------------------------- many rows per expert
-
-constexpr int kTileThreads = 256;
-constexpr int64_t kTileMinRows = 64;  // rows per expert, on average, from which the tile kernels are taken
-
-// The tile's rows of x.
-__device__ __forceinline__ TileTokens tile_tokens(const GroupedArgs& a, const RowTile& t, int width) {
-  const int row_bytes = (int)a.x.ld * 2;
-  return {make_rsrc((const uint16_t*)a.x.p + (int64_t)t.row0 * a.x.ld,
-                    (uint32_t)(t.rows - 1) * (uint32_t)row_bytes + (uint32_t)width * 2u),
-          row_bytes};
-}
-
 // The export of one expert as range-checked buffers.
 struct ExpertBuffers {
   __amdgpu_buffer_rsrc_t codes, steps, zeros;
@@ -253,6 +74,473 @@ __device__ __forceinline__ ExpertBuffers expert_buffers(const GroupedArgs& a, in
                                             0x00020000),
           __builtin_amdgcn_make_buffer_rsrc((void*)(a.steps + row * G), (short)0, a.d_out * G * 2, 0x00020000),
           __builtin_amdgcn_make_buffer_rsrc((void*)(a.zeros + row * GZ), (short)0, a.d_out * GZ, 0x00020000)};
+}
+
+// act(g) * u in float32
+__device__ __forceinline__ float gated(float g, float u, int mode) {
+  const float a = mode == AWQ_GROUPED_GATED_SILU ? g / (1.0f + __expf(-g)) : (g <= 0.0f ? 0.0f : g);  // NaN stays
+  return a * u;
+}
+
+// ---------------------------------------------------------------- a handful of rows per expert
+
+// Up to 16 rows of one expert against all of its weights, read once at the memory's rate. The tile's rows lie in
+// LDS whole, brought there by DMA. A wave multiplies 32 output rows (GATED: 16 of the gate and 16 of the up
+// matrix) by every KS-th chunk of 8 groups: it keeps the codes of kRing groups in flight in registers, and one load
+// brings a row's eight steps. With the rows in LDS the codes are the only loads that a wave waits for (the counter
+// of outstanding loads completes in issue order, so a load of activations behind codes would wait for these too),
+// and no load sits behind a branch, where the compiler would wait for it at once. The KS waves' partial products
+// are added at the end, in wave order.
+constexpr int kRing = 2;
+constexpr int kChunkGroups = 8;
+constexpr int kStreamWaves = 4;
+constexpr int kStreamLds = 64 << 10;  // bytes of rows in LDS: two blocks on a compute unit
+
+// Rows of d_in inputs that a tile holds in LDS.
+int stream_rows(int d_in) {
+  const int rows = kStreamLds / (2 * d_in);
+  return rows < 16 ? rows : 16;
+}
+
+struct __attribute__((packed, aligned(2))) Steps8 {
+  uint32_t s[4];
+};
+struct __attribute__((packed, aligned(1))) Zeros8 {
+  uint32_t z;
+};
+
+// A lane's place in one expert's export: its part (kq = lane / 16) of the codes of two output rows, one of each tile
+// of 16, and their steps and zero points, eight groups at a time.
+struct LaneRows {
+  const uint8_t* codes;
+  const uint16_t* steps;
+  const uint8_t* zeros;
+  int G, GZ, last_s, last_z;
+  int row[2];
+  uint32_t coff[2];
+  struct Params {
+    Steps8 s[2];
+    Zeros8 z[2];
+  };
+  // col0: the first column of y; GATED: row 0 of the gate, row 1 of the up matrix
+  template <bool GATED>
+  __device__ __forceinline__ void init(const GroupedArgs& a, int expert, int col0) {
+    const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
+    const int width = GATED ? a.d_out / 2 : a.d_out;
+    G = a.d_in / kGroup;
+    GZ = (G + 1) / 2;
+    const int64_t row_e = (int64_t)expert * a.d_out, rest = (int64_t)(a.n_experts - expert) * a.d_out;
+    codes = a.codes + row_e * (a.d_in / 2);
+    steps = a.steps + row_e * G;
+    zeros = a.zeros + row_e * GZ;
+    // the last places from which a load of eight does not pass the tensor's end
+    last_s = (int)min(rest * G - 8, (int64_t)0x7FFFFFFF);
+    last_z = (int)min(rest * GZ - 4, (int64_t)0x7FFFFFFF);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      row[j] = min(col0 + (GATED ? 0 : 16 * j) + n, width - 1) + (GATED ? j * width : 0);
+      coff[j] = (uint32_t)row[j] * (uint32_t)(a.d_in / 2) + kq * 16;
+    }
+  }
+  __device__ __forceinline__ void load_codes(int g, uint4 (&c)[2]) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      c[j] = *reinterpret_cast<const uint4*>(codes + (int64_t)g * (kGroup / 2) + coff[j]);
+  }
+  // of groups g0 .. g0 + 7; what lies behind the row's last group is not used
+  __device__ __forceinline__ void load_params(int g0, Params& p) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      p.s[j] = *reinterpret_cast<const Steps8*>(steps + min(row[j] * G + g0, last_s));
+      p.z[j] = *reinterpret_cast<const Zeros8*>(zeros + min(row[j] * GZ + (g0 >> 1), last_z));
+    }
+  }
+  // moves the elements of a load that started early, at the tensor's end, to their places
+  __device__ __forceinline__ void place_params(int g0, Params& p) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int ls = max(row[j] * G + g0 - last_s, 0), lz = max(row[j] * GZ + (g0 >> 1) - last_z, 0);
+      if (__ballot(ls | lz)) {
+        for (int k = 0; k < ls; ++k) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p.s[j].s[i] = (p.s[j].s[i] >> 16) | (i < 3 ? p.s[j].s[i + 1] << 16 : 0u);
+        }
+        p.z[j].z >>= 8 * lz;
+      }
+    }
+  }
+  // the constants of group u of eight, row j
+  static __device__ __forceinline__ MixParams mix(const Params& p, int j, int u) {
+    const float st = (float)__builtin_bit_cast(_Float16, (uint16_t)(p.s[j].s[u / 2] >> (16 * (u & 1))));
+    const int z = (p.z[j].z >> (4 * u)) & 15;
+    return {st, -(float)(1024 + z) * st, st * 0.0625f, -(float)(64 + z) * st};
+  }
+};
+
+// Stores a wave's 16 MT rows x 32 output rows (GATED: x 16 columns) from row r0 of the tile on.
+template <int KIND, typename OutT, bool GATED, int MT>
+__device__ __forceinline__ void store_rows(const GroupedArgs& a, const RowTile& t, int col0, const f32x4 (&acc)[MT][2]) {
+  const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
+  const int width = GATED ? a.d_out / 2 : a.d_out;
+  OutT* y = (OutT*)a.y.p + (int64_t)t.row0 * a.y.ld;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < (GATED ? 1 : 2); ++j) {
+      const int c = col0 + 16 * j + n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 16 * m + 4 * kq + i;
+        const float v = GATED ? gated(acc[m][0][i], acc[m][1][i], a.mode) : acc[m][j][i];
+        if (c < width && r < t.rows) y[(int64_t)r * a.y.ld + c] = to_out<OutT>(v, KIND);
+      }
+    }
+}
+
+template <int KIND, typename OutT, bool GATED, int KS>
+__global__ __launch_bounds__(64 * kStreamWaves, 5) void grouped_stream_kernel(GroupedArgs a, int tile_rows) {
+  constexpr int W = kStreamWaves, CI = W / KS;  // columns of 32 output rows per block
+  constexpr int D = kRing, C = kChunkGroups;
+  extern __shared__ __attribute__((aligned(1024))) char xs[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowTile t;
+  if (!find_tile(a.offsets, a.n_experts, a.n_rows, tile_rows, blockIdx.y, t)) return;
+  const int n = lane & 15, kq = lane >> 4;
+  const int ks = wave % KS, item = blockIdx.x * CI + wave / KS;
+  const int G = a.d_in / kGroup, col0 = item * (GATED ? 16 : 32);
+
+  // the rows on their way to LDS, row after row in 16-byte chunks; the 16 chunks of a group's slice XOR-swizzled by
+  // the row, so that 16 lanes that read one chunk of 16 rows find distinct banks
+  {
+    const int row_chunks = a.d_in / 8, all = t.rows * row_chunks, row_bytes = (int)a.x.ld * 2;
+    const uint32_t inverse = ((1u << 24) + row_chunks - 1) / row_chunks;  // p / row_chunks for p < 4096, exactly
+    const i32x4 xr = make_rsrc((const uint16_t*)a.x.p + (int64_t)t.row0 * a.x.ld,
+                               (uint32_t)(t.rows - 1) * (uint32_t)row_bytes + (uint32_t)a.d_in * 2u);
+    const uint32_t base = lds_address(xs);
+    for (int p0 = wave * 64; p0 < all; p0 += 64 * W) {
+      const int p = p0 + lane, r = (int)(__umul24(p, inverse) >> 24);  // r == rows past the last: out of range, zeros
+      const int s = p - r * row_chunks;
+      dma_load16(xr, __builtin_amdgcn_readfirstlane(base + p0 * 16),
+                 r * row_bytes + ((s & ~15) | ((s ^ r) & 15)) * 16, 0);
+    }
+  }
+
+  LaneRows w;
+  w.init<GATED>(a, t.expert, col0);
+  // this wave's groups: every KS-th chunk of C, the last chunk possibly short; a wave without any reads group 0
+  const int chunks = (G + C - 1) / C;
+  const int mine = chunks > ks ? (chunks - ks + KS - 1) / KS : 0;
+  const bool has_last = mine > 0 && (chunks - 1) % KS == ks;
+  const int n_groups = mine * C - (has_last ? chunks * C - G : 0);
+  auto group_of = [&](int i) { return (ks + (i / C) * KS) * C + i % C; };
+  uint4 cw[D][2];
+  auto load_codes = [&](int u, int i) {  // past the last group it is read again, and not used
+    w.load_codes(min(group_of(max(min(i, n_groups - 1), 0)), G - 1), cw[u]);
+  };
+  LaneRows::Params pr, pr_next;
+  w.load_params(min(ks * C, G - 1), pr);
+#pragma unroll
+  for (int u = 0; u < D; ++u) load_codes(u, u);
+  // the first codes are here: so are this wave's rows, whose loads went out before
+  asm volatile("" : "+v"(cw[0][0].x), "+v"(cw[0][1].x)::"memory");
+  __syncthreads();
+
+  const uint32_t magic = 0x64006400u;  // float16 1024 in both halves
+  const int xrow = min(n, t.rows - 1);
+  const char* xl = xs + xrow * a.d_in * 2;
+  int slot[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) slot[s] = ((4 * kq + s) ^ (xrow & 15)) << 4;
+  f32x4 acc[1][2] = {{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}};
+  for (int i0 = 0; i0 < n_groups; i0 += C) {
+    const int g0 = (ks + (i0 / C) * KS) * C;
+    w.load_params(min(g0 + KS * C, G - 1), pr_next);
+    w.place_params(g0, pr);
+    const char* xc = xl + g0 * (kGroup * 2);
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      if (i0 + u < n_groups) {  // wave-uniform
+        uint4 x[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[s] = *reinterpret_cast<const uint4*>(xc + u * (kGroup * 2) + slot[s]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const MixParams p = LaneRows::mix(pr, j, u);
+          const uint32_t q[4] = {cw[u % D][j].x, cw[u % D][j].y, cw[u % D][j].z, cw[u % D][j].w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) acc[0][j] = mma<KIND>(x[s], dequant8_mix<KIND>(q[s], p, magic), acc[0][j]);
+        }
+      }
+      load_codes(u % D, i0 + u + D);
+    }
+    pr = pr_next;
+  }
+
+  if constexpr (KS > 1) {
+    __syncthreads();  // the rows have been read: their place takes the partial products
+    f32x4* red = reinterpret_cast<f32x4*>(xs);
+    red[(wave * 2) * 64 + lane] = acc[0][0];
+    red[(wave * 2 + 1) * 64 + lane] = acc[0][1];
+    __syncthreads();
+    if (ks != 0) return;
+#pragma unroll
+    for (int k = 1; k < KS; ++k) {
+      acc[0][0] += red[((wave + k) * 2) * 64 + lane];
+      acc[0][1] += red[((wave + k) * 2 + 1) * 64 + lane];
+    }
+  }
+  store_rows<KIND, OutT, GATED, 1>(a, t, col0, acc);
+}
+
+// ---------------------------------------------------------------- some tens of rows per expert
+
+// 16 MT rows of one expert against its weights: each wave streams the codes of 32 output rows (GATED: 16 and 16)
+// through registers as above, each dequantized fragment multiplying MT row tiles. The rows come through LDS a group
+// (128 inputs) at a time, by DMA two groups ahead into a ring of four stages. Loads complete in issue order, and a
+// group's codes are sent for right behind its rows: with the codes in hand, so is the wave's share of the rows.
+template <int KIND, typename OutT, bool GATED, int W, int MT>
+__global__ __launch_bounds__(64 * W) void grouped_mid_kernel(GroupedArgs a) {
+  constexpr int C = kChunkGroups, kStages = 4, kStageBytes = 16 * MT * 256;
+  __shared__ __attribute__((aligned(1024))) char xs[kStages * kStageBytes];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowTile t;
+  if (!find_tile(a.offsets, a.n_experts, a.n_rows, 16 * MT, blockIdx.y, t)) return;
+  const int n = lane & 15, kq = lane >> 4;
+  const int G = a.d_in / kGroup;
+  const int col0 = (blockIdx.x * W + wave) * (GATED ? 16 : 32);
+
+  // DMA: wave w brings the kilobytes w, w + W, ... of a stage, four rows each; the 16 chunks of a row's slice are
+  // XOR-swizzled by the row. Rows past the tile's last read zeros.
+  const int row_bytes = (int)a.x.ld * 2;
+  const i32x4 xr = make_rsrc((const uint16_t*)a.x.p + (int64_t)t.row0 * a.x.ld,
+                             (uint32_t)(t.rows - 1) * (uint32_t)row_bytes + (uint32_t)a.d_in * 2u);
+  constexpr int kLoads = 4 * MT / W > 0 ? 4 * MT / W : 1;
+  const bool brings = wave < 4 * MT;
+  int voff[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = 4 * (wave + i * W) + (lane >> 4);
+    voff[i] = r * row_bytes + (((lane & 15) ^ (r & 15)) << 4);
+  }
+  const uint32_t base = lds_address(xs);
+  auto bring = [&](int g, int stage) {
+    if (brings && g < G) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        dma_load16(xr, __builtin_amdgcn_readfirstlane(base + stage * kStageBytes + (wave + i * W) * 1024), voff[i],
+                   g * (kGroup * 2));
+    }
+  };
+
+  LaneRows w;
+  w.init<GATED>(a, t.expert, col0);
+  LaneRows::Params pr, pr_next;
+  uint4 cw[2][2];
+  w.load_params(0, pr);
+  bring(0, 0);
+  w.load_codes(0, cw[0]);
+  bring(1, 1);
+  w.load_codes(min(1, G - 1), cw[1]);
+
+  const uint32_t magic = 0x64006400u;  // float16 1024 in both halves
+  const char* xl = xs + n * 256;
+  int slot[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) slot[s] = ((4 * kq + s) ^ n) << 4;
+  f32x4 acc[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int g0 = 0; g0 < G; g0 += C) {
+    w.load_params(min(g0 + C, G - 1), pr_next);
+    w.place_params(g0, pr);
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      if (g0 + u < G) {  // block-uniform
+        // the codes of group g0 + u are here, and this wave's rows of it; then every wave's. The stage that the
+        // next rows go to was last read two groups ago.
+        asm volatile("" : "+v"(cw[u & 1][0].x), "+v"(cw[u & 1][1].x)::"memory");
+        __syncthreads();
+        uint4 c[2] = {cw[u & 1][0], cw[u & 1][1]};
+        bring(g0 + u + 2, (u + 2) & 3);
+        w.load_codes(min(g0 + u + 2, G - 1), cw[u & 1]);
+        const MixParams p[2] = {LaneRows::mix(pr, 0, u), LaneRows::mix(pr, 1, u)};
+        const char* xc = xl + (u & 3) * kStageBytes;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint4 x[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) x[m] = *reinterpret_cast<const uint4*>(xc + m * 4096 + slot[s]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t q = s == 0 ? c[j].x : s == 1 ? c[j].y : s == 2 ? c[j].z : c[j].w;
+            const uint4 b = dequant8_mix<KIND>(q, p[j], magic);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[m][j] = mma<KIND>(x[m], b, acc[m][j]);
+          }
+        }
+      }
+    }
+    pr = pr_next;
+  }
+  store_rows<KIND, OutT, GATED, MT>(a, t, col0, acc);
+}
+
+// ---------------------------------------------------------------- the gradient with respect to the rows
+
+// Lane e of each row of 16 lanes, in all of the row's lanes.
+template <int E>
+__device__ __forceinline__ float row_bcast(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x150 + E, 0xF, 0xF, false));
+}
+
+// Up to some tens of rows per expert: 16 MT rows of d_x x one group's 128 columns per block, whose eight waves take
+// every eighth block of 32 output rows o and add their products at the end, in a fixed order. Lane n = l mod 16 of
+// lane group kq reads, for each of its eight k = 8 kq + e, the word of row o + k that holds columns 8 n .. 8 n + 7, so
+// that its eight column tiles j (column 8 n + j in column place n) each find their eight consecutive k in the lane's
+// own registers: the transposition costs no exchange. Lane n also brings the step and zero point of row o + 8 kq + n mod 8,
+// which the lanes of its group take from it. Everything for the next block is loaded before this one is multiplied.
+constexpr int kBackwardWaves = 8;
+
+template <int KIND, typename OutT, int MT>
+__global__ __launch_bounds__(64 * kBackwardWaves) void grouped_backward_mid_kernel(GroupedArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowTile t;
+  if (!find_tile(a.offsets, a.n_experts, a.n_rows, 16 * MT, blockIdx.y, t)) return;
+  const int G = a.d_in / kGroup, GZ = (G + 1) / 2, row_bytes = a.d_in / 2;
+  const int g = blockIdx.x;
+  const int n = lane & 15, kq = lane >> 4;
+  const ExpertBuffers buf = expert_buffers(a, t.expert);
+  const uint16_t* xrow[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    xrow[m] = (const uint16_t*)a.x.p + (int64_t)(t.row0 + min(16 * m + n, t.rows - 1)) * a.x.ld + 8 * kq;
+  f32x4 acc[MT][8];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  struct Block {
+    uint32_t w[8], s, z;
+    uint4 x[MT];
+  };
+  // weights of rows past d_out lie past the expert's buffers and read as zero
+  auto load_weights = [&](int b, Block& v) {
+    const uint32_t at = (uint32_t)(32 * b + 8 * kq) * (uint32_t)row_bytes + (uint32_t)(g * (kGroup / 2) + 4 * n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v.w[e] = __builtin_amdgcn_raw_buffer_load_b32(buf.codes, (int)(at + (uint32_t)(e * row_bytes)), 0, 0);
+    const int o = 32 * b + 8 * kq + (n & 7);
+    v.s = __builtin_amdgcn_raw_buffer_load_b16(buf.steps, (o * G + g) * 2, 0, 0);
+    v.z = __builtin_amdgcn_raw_buffer_load_b8(buf.zeros, o * GZ + (g >> 1), 0, 0);
+  };
+  auto load = [&](int b, Block& v) {
+    load_weights(b, v);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) v.x[m] = *reinterpret_cast<const uint4*>(xrow[m] + 32 * b);
+  };
+  const uint32_t magic = 0x64006400u;  // float16 1024 in both halves
+  auto multiply = [&](const Block& v) {
+    const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)v.s);
+    const float c = -(float)(1024 + ((v.z >> (4 * (g & 1))) & 15)) * s;  // exact, as in MixParams
+    const float st[8] = {row_bcast<0>(s), row_bcast<1>(s), row_bcast<2>(s), row_bcast<3>(s),
+                         row_bcast<4>(s), row_bcast<5>(s), row_bcast<6>(s), row_bcast<7>(s)};
+    const float c0[8] = {row_bcast<0>(c), row_bcast<1>(c), row_bcast<2>(c), row_bcast<3>(c),
+                         row_bcast<4>(c), row_bcast<5>(c), row_bcast<6>(c), row_bcast<7>(c)};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float lo[8], hi[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const f16x2_t h = __builtin_bit_cast(f16x2_t, and_or(v.w[e] >> (4 * q), 0x000F000Fu, magic));
+        lo[e] = fmaf((float)h.x, st[e], c0[e]);
+        hi[e] = fmaf((float)h.y, st[e], c0[e]);
+      }
+      const uint4 bl = make_uint4(pack2(lo[0], lo[1], KIND), pack2(lo[2], lo[3], KIND), pack2(lo[4], lo[5], KIND),
+                                  pack2(lo[6], lo[7], KIND));
+      const uint4 bh = make_uint4(pack2(hi[0], hi[1], KIND), pack2(hi[2], hi[3], KIND), pack2(hi[4], hi[5], KIND),
+                                  pack2(hi[6], hi[7], KIND));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        acc[m][q] = mma<KIND>(v.x[m], bl, acc[m][q]);
+        acc[m][q + 4] = mma<KIND>(v.x[m], bh, acc[m][q + 4]);
+      }
+    }
+  };
+  const int whole = a.d_out / 32;
+  Block now, next;
+  int b = wave;
+  if (b < whole) load(b, now);
+  for (; b < whole; b += kBackwardWaves) {
+    load(min(b + kBackwardWaves, whole - 1), next);  // past the last one it is read again, and not used
+    multiply(now);
+    now = next;
+  }
+  if (b == whole && a.d_out % 32) {  // the block that d_out cuts: what lies behind it in x is not read
+    load_weights(b, now);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      uint32_t q[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (32 * b + 8 * kq + e < a.d_out) q[e >> 1] |= (uint32_t)xrow[m][32 * b + e] << (16 * (e & 1));
+      now.x[m] = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+    multiply(now);
+  }
+  // waves h .. 2 h - 1 hand their products to waves 0 .. h - 1
+  f32x4* const red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+  for (int h = kBackwardWaves / 2; h >= 1; h /= 2) {
+    if (h < kBackwardWaves / 2) __syncthreads();
+    if (wave >= h && wave < 2 * h) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) red[(((wave - h) * MT + m) * 8 + j) * 64 + lane] = acc[m][j];
+    }
+    __syncthreads();
+    if (wave < h) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[m][j] += red[((wave * MT + m) * 8 + j) * 64 + lane];
+    }
+  }
+  if (wave != 0) return;
+  OutT* y = (OutT*)a.y.p;
+  struct __attribute__((packed, aligned(sizeof(OutT)))) Eight {
+    OutT v[8];
+  };
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 16 * m + 4 * kq + i;
+      Eight o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o.v[j] = to_out<OutT>(acc[m][j][i], KIND);
+      if (r < t.rows) *reinterpret_cast<Eight*>(y + (int64_t)(t.row0 + r) * a.y.ld + g * kGroup + 8 * n) = o;
+    }
+}
+
+// ---------------------------------------------------------------- many rows per expert
+
+constexpr int kTileThreads = 256;
+
+// The tile's rows of x.
+__device__ __forceinline__ TileTokens tile_tokens(const GroupedArgs& a, const RowTile& t, int width) {
+  const int row_bytes = (int)a.x.ld * 2;
+  return {make_rsrc((const uint16_t*)a.x.p + (int64_t)t.row0 * a.x.ld,
+                    (uint32_t)(t.rows - 1) * (uint32_t)row_bytes + (uint32_t)width * 2u),
+          row_bytes};
 }
 
 // 256 rows x 256 output rows of one expert (the tile loop of w4a16_tile.h); a tile of at most 128 rows takes
@@ -461,35 +749,88 @@ hipError_t over_tiles(int64_t tiles, F f) {
   return hipSuccess;
 }
 
-template <int KIND, typename OutT>
+// The forward kernels by the rows that an expert has on average (n_rows / n_experts; the split itself is known on
+// the device alone, and any split is right with any of them). Measured with 8 experts of 4096 x 22016 (gate and up),
+// all of them used, us:
+//   rows per expert     1     4    16    32    64   128   256
+//   stream             72   108   207   358
+//   mid, 1 x 16 rows   72    95   125   192
+//   mid, 2 x 16 rows   87   109   113   153
+//   mid, 4 x 16 rows  103   122   127   131   192   324   558
+//   tile              232   239   242   245   250   335   540
+// Where tiles and columns make few waves, the stream kernel's split of the contraction counts more: one token's 2 of
+// these 8 experts 26.7 against 32.4, of 11008 x 4096 down projections 15.9 against 50.
+constexpr int kTileMinRows = 144;   // tile kernels from here
+constexpr int kMid4MinRows = 24;    // 4 x 16 rows
+constexpr int kMid2MinRows = 5;     // 2 x 16 rows
+constexpr int64_t kFewWaves = 4096;
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+template <int KIND, typename OutT, bool GATED>
 hipError_t launch_forward(const GroupedArgs& a, hipStream_t st) {
-  const bool gate = a.mode != AWQ_GROUPED_PLAIN;
-  const int width = gate ? a.d_out / 2 : a.d_out;
-  if (a.n_rows >= kTileMinRows * a.n_experts) {
+  const int width = GATED ? a.d_out / 2 : a.d_out;
+  const int items = GATED ? (width + 15) / 16 : (width + 31) / 32;  // columns of 32 output rows
+  const int64_t used = a.n_rows < a.n_experts ? a.n_rows : a.n_experts;
+  auto at_least = [&](int rows) { return a.n_rows >= (int64_t)rows * a.n_experts; };
+  // (the small kernels load eight steps at a time: a smaller tensor of steps takes the tile kernel)
+  if (at_least(kTileMinRows) || (int64_t)a.n_experts * a.d_out * (a.d_in / kGroup) < 8) {
     const int tiles_m = (int)most_tiles(a.n_rows, a.n_experts, kTileTok);
-    const int tiles_n = gate ? (width + 127) / 128 : (width + 255) / 256;
+    const int tiles_n = GATED ? (width + 127) / 128 : (width + 255) / 256;
     return over_tiles((int64_t)tiles_m * tiles_n, [&](int first, dim3 grid) {
-      if (gate)
-        hipLaunchKernelGGL((grouped_tile_kernel<KIND, OutT, true>), grid, dim3(kTileThreads), 0, st, a, tiles_m, tiles_n,
-                           first);
-      else
-        hipLaunchKernelGGL((grouped_tile_kernel<KIND, OutT, false>), grid, dim3(kTileThreads), 0, st, a, tiles_m,
-                           tiles_n, first);
+      hipLaunchKernelGGL((grouped_tile_kernel<KIND, OutT, GATED>), grid, dim3(kTileThreads), 0, st, a, tiles_m, tiles_n,
+                         first);
     });
   }
-  const dim3 block(64 * kSmallWaves);
-  const unsigned gy = (unsigned)most_tiles(a.n_rows, a.n_experts, 16);
-  if (gate)
-    hipLaunchKernelGGL((grouped_small_kernel<KIND, OutT, 2, 1, true>), dim3((width + 15) / 16, gy), block, 0, st, a);
-  else
-    hipLaunchKernelGGL((grouped_small_kernel<KIND, OutT, 2, 1, false>), dim3((width + 31) / 32, gy), block, 0, st, a);
+  const int rows = stream_rows(a.d_in);
+  if (rows >= 1 && !at_least(rows + 1) && used * items < kFewWaves) {
+    const int chunks = (a.d_in / kGroup + kChunkGroups - 1) / kChunkGroups;
+    const int64_t tiles = most_tiles(a.n_rows, a.n_experts, rows);
+    const int lds = ((rows < a.n_rows ? rows : a.n_rows) * 2 * a.d_in + 1023) / 1024 * 1024;
+    auto go = [&](auto split) {
+      constexpr int W = kStreamWaves, KS = decltype(split)::value, CI = W / KS;
+      hipLaunchKernelGGL((grouped_stream_kernel<KIND, OutT, GATED, KS>), dim3((items + CI - 1) / CI, (unsigned)tiles),
+                         dim3(64 * W), lds > W * 2048 ? lds : W * 2048, st, a, rows);
+    };
+    if (chunks >= 4) go(Int<4>{});
+    else if (chunks >= 2) go(Int<2>{});
+    else go(Int<1>{});
+    return hipGetLastError();
+  }
+  auto go = [&](auto waves, auto row_tiles) {
+    constexpr int W = decltype(waves)::value, MT = decltype(row_tiles)::value;
+    hipLaunchKernelGGL((grouped_mid_kernel<KIND, OutT, GATED, W, MT>),
+                       dim3((items + W - 1) / W, (unsigned)most_tiles(a.n_rows, a.n_experts, 16 * MT)), dim3(64 * W), 0,
+                       st, a);
+  };
+  if (at_least(kMid4MinRows)) go(Int<8>{}, Int<4>{});
+  else if (at_least(kMid2MinRows)) go(Int<4>{}, Int<2>{});
+  else go(Int<4>{}, Int<1>{});
   return hipGetLastError();
 }
 
+// The gradient's kernels by the rows per expert. Measured with 8 experts of 22016 x 4096, all of them used, us:
+//   rows per expert     4    16    32    64   128   256
+//   mid, 1 x 16 rows  169   249   323   456
+//   mid, 2 x 16 rows  171   167   277   356   540
+//   mid, 4 x 16 rows  159   167   174   322   455   707
+//   tile              382   382   383   386   478   522
+// The tile kernel's time is a tile's whole contraction as long as its tiles do not fill the compute units; 64 experts
+// of 2048 x 2048 with 64 rows each, which do, take it 95 against 124.
+constexpr int kBackwardTileMinRows = 144;
+constexpr int kBackwardTileMinRowsFull = 48;  // where the tiles fill the compute units
+constexpr int64_t kFullTiles = 256;
+constexpr int kBackwardMid4MinRows = 24;
+constexpr int kBackwardMid2MinRows = 10;
+
 template <int KIND, typename OutT>
 hipError_t launch_backward(const GroupedArgs& a, hipStream_t st) {
-  if (a.n_rows >= kTileMinRows * a.n_experts) {
-    const int tiles_m = (int)most_tiles(a.n_rows, a.n_experts, kTileTok), tiles_n = (a.d_in + 255) / 256;
+  auto at_least = [&](int rows) { return a.n_rows >= (int64_t)rows * a.n_experts; };
+  const int tiles_n = (a.d_in + 255) / 256;
+  const int64_t used = a.n_rows < a.n_experts ? a.n_rows : a.n_experts;
+  if (at_least(kBackwardTileMinRows) || (at_least(kBackwardTileMinRowsFull) && used * tiles_n >= kFullTiles)) {
+    const int tiles_m = (int)most_tiles(a.n_rows, a.n_experts, kTileTok);
     return over_tiles((int64_t)tiles_m * tiles_n, [&](int first, dim3 grid) {
       if ((a.d_out + 63) / 64 % 2 == 0)
         hipLaunchKernelGGL((grouped_backward_tile_kernel<KIND, OutT, true>), grid, dim3(kTileThreads), 0, st, a, tiles_m,
@@ -499,17 +840,28 @@ hipError_t launch_backward(const GroupedArgs& a, hipStream_t st) {
                            tiles_m, tiles_n, first);
     });
   }
-  const unsigned gy = (unsigned)most_tiles(a.n_rows, a.n_experts, 64);
-  hipLaunchKernelGGL((grouped_backward_simple_kernel<KIND, OutT, 4>), dim3((a.d_in / kGroup + 3) / 4, gy), dim3(256),
-                     0, st, a);
+  auto go = [&](auto row_tiles) {
+    constexpr int MT = decltype(row_tiles)::value;
+    hipLaunchKernelGGL((grouped_backward_mid_kernel<KIND, OutT, MT>),
+                       dim3(a.d_in / kGroup, (unsigned)most_tiles(a.n_rows, a.n_experts, 16 * MT)),
+                       dim3(64 * kBackwardWaves), MT * 32768, st, a);
+  };
+  if (at_least(kBackwardMid4MinRows)) go(Int<4>{});
+  else if (at_least(kBackwardMid2MinRows)) go(Int<2>{});
+  else go(Int<1>{});
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_w4a16_grouped(const GroupedArgs& a, int kind, bool y_f32, hipStream_t st) {
-  if (kind == 0) return y_f32 ? launch_forward<0, float>(a, st) : launch_forward<0, uint16_t>(a, st);
-  return y_f32 ? launch_forward<1, float>(a, st) : launch_forward<1, uint16_t>(a, st);
+  auto go = [&](auto k, auto out) {
+    constexpr int KIND = decltype(k)::value;
+    typedef decltype(out) OutT;
+    return a.mode == AWQ_GROUPED_PLAIN ? launch_forward<KIND, OutT, false>(a, st) : launch_forward<KIND, OutT, true>(a, st);
+  };
+  if (kind == 0) return y_f32 ? go(Int<0>{}, 0.f) : go(Int<0>{}, (uint16_t)0);
+  return y_f32 ? go(Int<1>{}, 0.f) : go(Int<1>{}, (uint16_t)0);
 }
 
 hipError_t launch_w4a16_grouped_backward(const GroupedArgs& a, int kind, bool y_f32, hipStream_t st) {

@@ -67,15 +67,22 @@ def exported_symbols() -> list[str]:
     return list(_SIGNATURES)
 
 
+# the raw handle of a device's current stream; the public call builds a Stream object, which costs a small call as much
+# as its launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn, dev, stream, *args) -> None:
     """Enqueues on `stream`, or on the current stream of the tensors' device, with that device current."""
-    if dev.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream() if stream is None else stream
-        binding._check(fn(*args, s.cuda_stream))
+    index = dev.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            s = torch.cuda.current_stream() if stream is None else stream
-            binding._check(fn(*args, s.cuda_stream))
+            status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if status:
+        binding._check(status)
 
 
 def _matrix(t, name: str, shape=None, dtype=None, device=None) -> tuple[int, int]:
@@ -109,6 +116,8 @@ def _output(t, name: str, shape, dtype, device):
 
 
 def _vector(t, name: str, dtype, n: int, device) -> int:
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == (n,) and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name} must be a vector of {n} elements")
     return _buf(t, name, dtype, n, device)
@@ -203,6 +212,8 @@ def awq_block_norm_backward(y, residual: torch.Tensor, d_res_out, d_h, w_pre=Non
 
 def _slots(t, name: str, dtype, n=None, k=None, device=None) -> int:
     """Pointer of a contiguous [n_tokens, top_k] tensor."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == (n, k) and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or (n is not None and tuple(t.shape) != (n, k)):
         raise ValueError(f"{name} must be a [n_tokens, top_k] matrix" + ("" if n is None else f", here [{n}, {k}]"))
     return _buf(t, name, dtype, t.numel(), device)
@@ -220,15 +231,17 @@ def awq_moe_sort(expert_ids: torch.Tensor, n_experts: int, workspace=None, out=N
     n, k = expert_ids.shape
     dev = expert_ids.device
     out = out or {}
-    res = {}
+    res, ptrs = {}, []
     for name, shape in (("offsets", (n_experts + 1,)), ("order", (n * k,)), ("position", (n, k))):
         o = out.get(name)
         if o is None:
             o = torch.empty(shape if n_experts > 0 else (0,), dtype=torch.int32, device=dev)
-        elif tuple(o.shape) != shape:
+            ptrs.append(o.data_ptr())
+        elif not isinstance(o, torch.Tensor) or o.shape != shape:
             raise ValueError(f"{name} must have shape {list(shape)}")
+        else:
+            ptrs.append(_buf(o, name, torch.int32, 0, dev))
         res[name] = o
-    ptrs = [_buf(o, name, torch.int32, 0, dev) for name, o in res.items()]
     nb, pw = lib.awq_moe_sort_workspace_bytes(n, k, n_experts), None
     if nb:
         workspace = _workspace(nb, dev, workspace)
