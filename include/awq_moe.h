@@ -27,7 +27,8 @@
  *     otherwise. Sums, norms and products are held in float32 and rounded once, to nearest even.
  *   - A slot is t * top_k + j (token t, choice j); there are n_tokens * top_k of them, at most
  *     AWQ_MAX_SLOTS. expert_ids holds one expert per slot as int32 or int64 (id_bytes 4 or 8); an id
- *     outside [0, n_experts) drops the slot (a padded token, a full expert).
+ *     outside [0, n_experts) drops the slot (a padded token, a full expert). No tokens or rows at all is
+ *     AWQ_ERR_NO_TOKENS; an expert may have none.
  *   - Offsets, positions and orders that a caller changes are checked on the device: an entry outside
  *     its range is skipped or clamped, never followed out of a buffer.
  *   - Outputs must not overlap inputs unless stated otherwise. Two calls may run at the same time

@@ -52,6 +52,7 @@ struct RouteArgs {
   bool ids64;
   const float* scales;
   int n_experts;
+  bool stream_out;  // gather, combine's gradient: the rows written are too many for the second-level caches
 };
 hipError_t launch_moe_gather(const RouteArgs& a, int dtype, CMat x, Mat rows, hipStream_t stream);
 // out[t] = sum_j (weights or 1) * (scales or 1) * rows[position]

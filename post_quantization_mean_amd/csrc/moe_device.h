@@ -94,13 +94,17 @@ __device__ __forceinline__ uint4 own_raw(uint4 u, int skip) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T>
+// STREAM: past the second-level caches.
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ void store_own(T* row, const Place<T>& p, const float (&v)[kVec<T>]) {
+  typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));  // at any element
   Chunk<T> c;
 #pragma unroll
   for (int k = 0; k < kVec<T>; ++k) c.v[k] = from_f32<T>(v[k]);
   if (p.skip == 0) {
-    *reinterpret_cast<Chunk<T>*>(row + p.at) = c;
+    Words* to = reinterpret_cast<Words*>(row + p.at);
+    if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(Words, c), to);
+    else *to = __builtin_bit_cast(Words, c);
   } else {
 #pragma unroll
     for (int k = 0; k < kVec<T>; ++k)

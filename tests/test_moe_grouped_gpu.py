@@ -79,6 +79,17 @@ def test_exact_arithmetic_bit_exact(moe, dtype, out, n_rows, e, d_in, d_out, bac
     assert not bad.any(), f"{int(bad.sum())} of {bad.size} differ, first at {np.argwhere(bad)[0]}"
 
 
+# many experts with few, some and tens of rows and outputs for thousands of waves; rows too long for shared memory;
+# experts' tiles that fill the compute units
+@pytest.mark.parametrize("n_rows,e,d_in,d_out", [(130, 40, 128, 3300), (300, 40, 128, 3300), (700, 40, 128, 3300),
+                                                 (1200, 40, 128, 3300), (3, 2, 34816, 20), (60, 4, 34816, 18),
+                                                 (3200, 64, 1024, 40), (3200, 64, 1024, 90)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_exact_arithmetic_of_many_experts_and_long_rows(moe, n_rows, e, d_in, d_out, backward):
+    test_exact_arithmetic_bit_exact(moe, "bf16", "same", n_rows, e, d_in, d_out, backward)
+    test_exact_arithmetic_bit_exact(moe, "f16", "f32", n_rows, e, d_in, d_out, backward)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("n_rows,e,d_in,d_out", [(3, 8, 4096, 66), (50, 4, 512, 130), (700, 3, 1280, 200), (2500, 2, 384, 300)])
 def test_real_values(moe, dtype, n_rows, e, d_in, d_out):

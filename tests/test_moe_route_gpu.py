@@ -109,6 +109,53 @@ def test_gather_and_combine(moe, dtype, n, k, e, d, scaled, strided):
     within(host(got), want, k * U * mag * (1 + hs) + hs * np.abs(want) * (1 + k * U) + U, "d_x")
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("n,k,d", [(4099, 4, 2051), (9001, 2, 1000), (16811, 1, 1024), (1100003, 1, 17), (300007, 2, 9),
+                                   (270011, 3, 3)])
+def test_many_rows(moe, dtype, n, k, d):
+    """Rows of more than 32 MiB, and tokens past one dimension of a grid, against torch in float64 on the device
+    (one factor or k terms each: the bounds of the test above)."""
+    print(f"[gpu route] many rows n={n} k={k} d={d} {dtype}", flush=True)
+    g = torch.Generator("cuda").manual_seed(n)
+    e, t, hs = 7, DTYPES[dtype], half_step(dtype)
+    ids = torch.randint(-1, e, (n, k), generator=g, device="cuda")
+    pos = moe.awq_moe_sort(ids, e)["position"]
+    scales = torch.rand((e, d), generator=g, device="cuda") + 0.5
+    x = torch.randn((n, d), generator=g, device="cuda").to(t)
+    w = torch.randn((n, k), generator=g, device="cuda")
+    at, kept = pos.clamp(min=0).long(), pos >= 0
+
+    def near(got, want, tol):
+        for a in range(0, len(want), 8192):
+            assert bool((torch.abs(got[a:a + 8192].double() - want[a:a + 8192]) <= tol[a:a + 8192]).all())
+
+    def rows_of(factor):  # the kept slots' rows from x and factors [n, d] per choice, fives elsewhere
+        want = torch.full((n * k, d), 5.0, dtype=torch.float64, device="cuda")
+        for j in range(k):
+            want[at[kept[:, j], j]] = (x.double() * factor(j))[kept[:, j]]
+        return want
+
+    for kw, factor in (({}, lambda j: 1.0), (dict(expert_ids=ids, in_scales=scales), lambda j: scales[ids[:, j].clamp(min=0)].double())):
+        want = rows_of(factor)
+        got = moe.awq_moe_gather(x, pos, out=torch.full((n * k, d), 5.0, dtype=t, device="cuda"), **kw)
+        near(got, want, (U + hs) * want.abs() * (1 + U) + U)
+        back = moe.awq_moe_gather_backward(got, pos, **kw)
+        terms = [torch.where(kept[:, j, None], got[at[:, j]].double() * factor(j), 0.0) for j in range(k)]
+        want, mag = sum(terms), sum(v.abs() for v in terms)
+        near(back, want, k * U * mag * (1 + hs) + hs * want.abs() * (1 + k * U) + U)
+    rows = got
+    out = moe.awq_moe_combine(rows, pos, w)
+    terms = [torch.where(kept[:, j, None], rows[at[:, j]].double() * w[:, j, None].double(), 0.0) for j in range(k)]
+    want, mag = sum(terms), sum(v.abs() for v in terms)
+    near(out, want, k * U * mag * (1 + hs) + hs * want.abs() * (1 + k * U) + U)
+    b = moe.awq_moe_combine_backward(x, rows, pos, w, out={"d_rows": torch.full((n * k, d), 5.0, dtype=t, device="cuda")})
+    want = rows_of(lambda j: w[:, j, None].double())
+    near(b["d_rows"], want, (U + hs) * want.abs() * (1 + U) + U)
+    for j in range(k):
+        terms = torch.where(kept[:, j, None], rows[at[:, j]].double() * x.double(), 0.0)
+        near(b["d_weights"][:, j:j + 1], terms.sum(1, keepdim=True), (d / 64 + 7) * U * terms.abs().sum(1, keepdim=True))
+
+
 def test_rows_past_the_buffer_and_bad_entries_are_skipped(moe):
     """position is the caller's to change: entries outside [0, n_rows), and ids outside the experts, are skipped."""
     x = torch.ones((3, 64), dtype=torch.float32, device="cuda")
