@@ -127,10 +127,11 @@ PARTS = [(pre, post, block, gate, d_res) for pre, post, block in ((True, False, 
          for gate in (None, "channel", "token") for d_res in (True, False) if (block or not gate) and (pre or d_res)]
 
 
+@pytest.mark.parametrize("n,d", [(5, 300), (3, 9003), (700, 7)])
 @pytest.mark.parametrize("pre,post,block,gate,with_d_res", PARTS)
-def test_parts_left_out(moe, pre, post, block, gate, with_d_res):
+def test_parts_left_out(moe, pre, post, block, gate, with_d_res, n, d):
     rng = np.random.default_rng(17)
-    v = _inputs(rng, 5, 300, gate)
+    v = _inputs(rng, n, d, gate)
     for name, there in (("w_pre", pre), ("w_post", post), ("y", block)):
         v[name] = v[name] if there else None
     t, v = _dev_inputs(v, "bf16")
@@ -138,17 +139,18 @@ def test_parts_left_out(moe, pre, post, block, gate, with_d_res):
     got = moe.awq_block_norm(t["y"], t["residual"], t["w_pre"], t["w_post"], t["gate"], -1.25, eps)
     assert sorted(got) == (["h"] if pre else []) + (["residual"] if block else [])
     _check_forward(got, v, -1.25, eps, "bf16")
-    d_res = dev(rng.normal(size=(5, 300)), "bf16") if with_d_res else None
-    d_h = dev(rng.normal(size=(5, 300)), "bf16") if pre else None
+    d_res = dev(rng.normal(size=(n, d)), "bf16") if with_d_res else None
+    d_h = dev(rng.normal(size=(n, d)), "bf16") if pre else None
     got = moe.awq_block_norm_backward(t["y"], t["residual"], d_res, d_h, t["w_pre"], t["w_post"], t["gate"], -1.25, eps)
     _check_backward(got, v, {"d_res": None if d_res is None else host(d_res), "d_h": None if d_h is None else host(d_h)},
                     -1.25, eps, "bf16")
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-def test_pitched_unaligned_rows_and_in_place(moe, dtype):
+@pytest.mark.parametrize("d", [1037, 8221])
+def test_pitched_unaligned_rows_and_in_place(moe, dtype, d):
     rng = np.random.default_rng(23)
-    n, d, ld, eps = 6, 1037, 1043, float(np.float32(1e-6))
+    n, ld, eps = 6, d + 6, float(np.float32(1e-6))
     t, v = _dev_inputs(_inputs(rng, n, d, "token"), dtype)
     y, _ = pitched(v["y"], dtype, ld)
     r, rbuf = pitched(v["residual"], dtype, ld + 2)
