@@ -107,7 +107,7 @@ def _matrix(t, name: str, shape=None, dtype=None, device=None) -> tuple[int, int
 def _output(t, name: str, shape, dtype, device):
     """A caller's output or a new one, with its pointer and pitch."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(*shape, dtype=dtype, device=device)  # sizes one by one: a tuple costs almost a microsecond more
         return t, t.data_ptr(), shape[1]
     p, ld = _matrix(t, name, shape, dtype, device)
     if ld < shape[1]:
@@ -212,7 +212,9 @@ def awq_block_norm_backward(y, residual: torch.Tensor, d_res_out, d_h, w_pre=Non
 
 def _slots(t, name: str, dtype, n=None, k=None, device=None) -> int:
     """Pointer of a contiguous [n_tokens, top_k] tensor."""
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == (n, k) and t.device == device and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.is_cuda and (t.dim() == 2 if n is None else t.shape == (n, k)) \
+            and (t.dtype in dtype if type(dtype) is tuple else t.dtype == dtype) \
+            and (device is None or t.device == device) and t.is_contiguous():
         return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or (n is not None and tuple(t.shape) != (n, k)):
         raise ValueError(f"{name} must be a [n_tokens, top_k] matrix" + ("" if n is None else f", here [{n}, {k}]"))
@@ -235,7 +237,7 @@ def awq_moe_sort(expert_ids: torch.Tensor, n_experts: int, workspace=None, out=N
     for name, shape in (("offsets", (n_experts + 1,)), ("order", (n * k,)), ("position", (n, k))):
         o = out.get(name)
         if o is None:
-            o = torch.empty(shape if n_experts > 0 else (0,), dtype=torch.int32, device=dev)
+            o = torch.empty(*(shape if n_experts > 0 else (0,)), dtype=torch.int32, device=dev)
             ptrs.append(o.data_ptr())
         elif not isinstance(o, torch.Tensor) or o.shape != shape:
             raise ValueError(f"{name} must have shape {list(shape)}")
@@ -332,7 +334,7 @@ def awq_moe_combine_backward(d_out: torch.Tensor, rows: torch.Tensor, position: 
     d_rows, po, ldo = _output(out.get("d_rows"), "d_rows", (n_rows, d), rows.dtype, dev)
     d_weights = out.get("d_weights")
     if d_weights is None:
-        d_weights = torch.empty((n, k), dtype=torch.float32, device=dev)
+        d_weights = torch.empty(n, k, dtype=torch.float32, device=dev)
     pdw = _slots(d_weights, "d_weights", torch.float32, n, k, dev)
     _call(lib.awq_moe_combine_backward, dev, stream, pd, ldd, pr, ldr, dt, n_rows, d, pp, pw, n, k, po, ldo, pdw)
     return {"d_rows": d_rows, "d_weights": d_weights}
