@@ -760,10 +760,22 @@ hipError_t over_tiles(int64_t tiles, F f) {
 //   tile              232   239   242   245   250   335   540
 // Where tiles and columns make few waves, the stream kernel's split of the contraction counts more: one token's 2 of
 // these 8 experts 26.7 against 32.4, of 11008 x 4096 down projections 15.9 against 50.
-constexpr int kTileMinRows = 144;   // tile kernels from here
+// The tile kernel's time is that of one tile's whole contraction as long as its 256 x 256 tiles do not fill the compute
+// units; with so few the 64-row kernel's many more blocks are faster. By the outputs in tiles, us, mid 4 / tile:
+//   1 expert of 4096 x 1024, 250 rows (4)  43 /  83      8 of 4096 x 4096, 160 rows (80)    79 /  95
+//   2 of 4096 x 4096, 250 rows (32)        47 /  87      8 of 4096 x 4096, 250 rows (125)   85 /  94
+//   2 of 4096 x 4096, 500 rows (64)        50 /  89      32 of 2048 x 2048, 160 rows (160)  69 /  68
+//   8 of 11008 x 1024, 500 rows (64)      128 / 220      8 of 4096 x 4096, 500 rows (250)  158 / 118
+constexpr int kTileMinRows = 144;   // tile kernels from here,
+constexpr int kTileMinTiles = 128;  // with so many tiles' outputs
 constexpr int kMid4MinRows = 24;    // 4 x 16 rows
 constexpr int kMid2MinRows = 5;     // 2 x 16 rows
 constexpr int64_t kFewWaves = 4096;
+// Waves of a 64-row block, which share its rows' loads, by the waves there are (estimated from the average), us with
+// 8 / 4 / 2 a block: 8 experts of 4096 x 4096, 250 rows (4096) 88 / 99 / 128, 120 rows (2048) 54 / 52 / 68, 60 rows
+// (1024) 50 / 38 / 37; 2 of 4096 x 1024, 120 rows (128) 43 / 32 / 30; 32 of 4096 x 512, 60 rows (512) 46 / 36 / 34, 120
+// rows (1024) 48 / 41 / 47.
+constexpr int64_t kMidWaves8 = 2048, kMidWaves4 = 512;  // more waves than these: 8, 4 a block
 
 template <int N>
 using Int = std::integral_constant<int, N>;
@@ -775,9 +787,10 @@ hipError_t launch_forward(const GroupedArgs& a, hipStream_t st) {
   const int64_t used = a.n_rows < a.n_experts ? a.n_rows : a.n_experts;
   auto at_least = [&](int rows) { return a.n_rows >= (int64_t)rows * a.n_experts; };
   // (the small kernels load eight steps at a time: a smaller tensor of steps takes the tile kernel)
-  if (at_least(kTileMinRows) || (int64_t)a.n_experts * a.d_out * (a.d_in / kGroup) < 8) {
+  const int tiles_n = GATED ? (width + 127) / 128 : (width + 255) / 256;
+  const bool fill = (int64_t)a.n_rows * tiles_n >= (int64_t)kTileMinTiles * kTileTok;
+  if ((at_least(kTileMinRows) && fill) || (int64_t)a.n_experts * a.d_out * (a.d_in / kGroup) < 8) {
     const int tiles_m = (int)most_tiles(a.n_rows, a.n_experts, kTileTok);
-    const int tiles_n = GATED ? (width + 127) / 128 : (width + 255) / 256;
     return over_tiles((int64_t)tiles_m * tiles_n, [&](int first, dim3 grid) {
       hipLaunchKernelGGL((grouped_tile_kernel<KIND, OutT, GATED>), grid, dim3(kTileThreads), 0, st, a, tiles_m, tiles_n,
                          first);
@@ -804,8 +817,12 @@ hipError_t launch_forward(const GroupedArgs& a, hipStream_t st) {
                        dim3((items + W - 1) / W, (unsigned)most_tiles(a.n_rows, a.n_experts, 16 * MT)), dim3(64 * W), 0,
                        st, a);
   };
-  if (at_least(kMid4MinRows)) go(Int<8>{}, Int<4>{});
-  else if (at_least(kMid2MinRows)) go(Int<4>{}, Int<2>{});
+  const int64_t waves = used * ((a.n_rows + 64 * used - 1) / (64 * used)) * items;
+  if (at_least(kMid4MinRows)) {
+    if (waves > kMidWaves8) go(Int<8>{}, Int<4>{});
+    else if (waves > kMidWaves4) go(Int<4>{}, Int<4>{});
+    else go(Int<2>{}, Int<4>{});
+  } else if (at_least(kMid2MinRows)) go(Int<4>{}, Int<2>{});
   else go(Int<4>{}, Int<1>{});
   return hipGetLastError();
 }
@@ -817,8 +834,12 @@ hipError_t launch_forward(const GroupedArgs& a, hipStream_t st) {
 //   mid, 4 x 16 rows  159   167   174   322   455   707
 //   tile              382   382   383   386   478   522
 // The tile kernel's time is a tile's whole contraction as long as its tiles do not fill the compute units; 64 experts
-// of 2048 x 2048 with 64 rows each, which do, take it 95 against 124.
+// of 2048 x 2048 with 64 rows each, which do, take it 95 against 124. By the outputs in tiles, us, mid 4 / tile:
+//   1 expert of 4096 x 1024, 250 rows (4)  27 /  91      8 of 4096 x 4096, 160 rows (80)     85 / 103
+//   2 of 4096 x 4096, 250 rows (32)        32 /  93      8 of 4096 x 4096, 250 rows (125)   113 / 100
+//   2 of 4096 x 4096, 500 rows (64)        60 /  96      32 of 2048 x 2048, 160 rows (160)  103 /  69
 constexpr int kBackwardTileMinRows = 144;
+constexpr int kBackwardTileMinTiles = 96;  // outputs of so many tiles
 constexpr int kBackwardTileMinRowsFull = 48;  // where the tiles fill the compute units
 constexpr int64_t kFullTiles = 256;
 constexpr int kBackwardMid4MinRows = 24;
@@ -829,7 +850,8 @@ hipError_t launch_backward(const GroupedArgs& a, hipStream_t st) {
   auto at_least = [&](int rows) { return a.n_rows >= (int64_t)rows * a.n_experts; };
   const int tiles_n = (a.d_in + 255) / 256;
   const int64_t used = a.n_rows < a.n_experts ? a.n_rows : a.n_experts;
-  if (at_least(kBackwardTileMinRows) || (at_least(kBackwardTileMinRowsFull) && used * tiles_n >= kFullTiles)) {
+  const bool fill = (int64_t)a.n_rows * tiles_n >= (int64_t)kBackwardTileMinTiles * kTileTok;
+  if ((at_least(kBackwardTileMinRows) && fill) || (at_least(kBackwardTileMinRowsFull) && used * tiles_n >= kFullTiles)) {
     const int tiles_m = (int)most_tiles(a.n_rows, a.n_experts, kTileTok);
     return over_tiles((int64_t)tiles_m * tiles_n, [&](int first, dim3 grid) {
       if ((a.d_out + 63) / 64 % 2 == 0)

@@ -82,7 +82,7 @@ def test_exact_arithmetic_bit_exact(moe, dtype, out, n_rows, e, d_in, d_out, bac
 # many experts with few, some and tens of rows and outputs for thousands of waves; rows too long for shared memory;
 # experts' tiles that fill the compute units
 @pytest.mark.parametrize("n_rows,e,d_in,d_out", [(130, 40, 128, 3300), (300, 40, 128, 3300), (700, 40, 128, 3300),
-                                                 (1200, 40, 128, 3300), (3, 2, 34816, 20), (60, 4, 34816, 18),
+                                                 (1200, 40, 128, 3300), (3, 2, 34816, 20), (60, 4, 34816, 18), (450, 9, 256, 2200),
                                                  (3200, 64, 1024, 40), (3200, 64, 1024, 90)])
 @pytest.mark.parametrize("backward", [False, True])
 def test_exact_arithmetic_of_many_experts_and_long_rows(moe, n_rows, e, d_in, d_out, backward):
