@@ -30,7 +30,8 @@
  *     outside [0, n_experts) drops the slot (a padded token, a full expert). No tokens or rows at all is
  *     AWQ_ERR_NO_TOKENS; an expert may have none.
  *   - Offsets, positions and orders that a caller changes are checked on the device: an entry outside
- *     its range is skipped or clamped, never followed out of a buffer.
+ *     its range is skipped or clamped, never followed out of a buffer. Two slots may name the same row where
+ *     rows are read (both count); a row that is written holds, element by element, one of the two values.
  *   - Outputs must not overlap inputs unless stated otherwise. Two calls may run at the same time
  *     unless they share a workspace or an output.
  */
