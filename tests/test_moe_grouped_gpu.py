@@ -56,6 +56,8 @@ def _plain_bound(x, W, off, K, backward, want, hs):
 SHAPES = [(1, 1, 128, 1), (1, 8, 256, 40), (2, 8, 4096, 64), (7, 3, 384, 300), (16, 1, 640, 33), (40, 60, 128, 272),
           (64, 4, 1152, 48), (100, 5, 256, 520), (300, 2, 384, 260), (513, 7, 128, 130), (1030, 3, 256, 264),
           (2100, 2, 640, 520), (4200, 12, 128, 96), (700, 2, 256, 64), (650, 2, 256, 40), (700, 1, 384, 192), (2100, 3, 128, 128)]
+# outputs of enough 256 x 256 tiles for these; odd and even steps of the contraction, tails below and above 128 rows
+SHAPES += [(16400, 3, 256, 520), (9000, 5, 640, 1100), (33000, 12, 128, 100), (11000, 3, 640, 520), (25700, 40, 128, 300)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -91,7 +93,8 @@ def test_exact_arithmetic_of_many_experts_and_long_rows(moe, n_rows, e, d_in, d_
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("n_rows,e,d_in,d_out", [(3, 8, 4096, 66), (50, 4, 512, 130), (700, 3, 1280, 200), (2500, 2, 384, 300)])
+@pytest.mark.parametrize("n_rows,e,d_in,d_out", [(3, 8, 4096, 66), (50, 4, 512, 130), (700, 3, 1280, 200), (2500, 2, 384, 300),
+                                                 (17000, 2, 384, 300)])
 def test_real_values(moe, dtype, n_rows, e, d_in, d_out):
     rng = np.random.default_rng(n_rows + d_out)
     for backward in (False, True):
@@ -107,7 +110,7 @@ def test_real_values(moe, dtype, n_rows, e, d_in, d_out):
 @pytest.mark.parametrize("act", ["silu", "relu"])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("n_rows,e,d_in,d_out", [(1, 2, 128, 2), (2, 8, 4096, 96), (30, 3, 640, 130), (90, 4, 256, 258),
-                                                 (300, 3, 384, 520), (1300, 4, 256, 258), (2600, 1, 128, 1030)])
+                                                 (300, 3, 384, 520), (1300, 4, 256, 258), (2600, 1, 128, 1030), (17000, 4, 256, 258), (34000, 1, 128, 130)])
 def test_gated(moe, act, dtype, n_rows, e, d_in, d_out):
     rng = np.random.default_rng(n_rows + d_in)
     kept = n_rows - n_rows // 20
@@ -127,7 +130,7 @@ def test_gated(moe, act, dtype, n_rows, e, d_in, d_out):
 
 def test_strided_rows_and_outputs(moe):
     rng = np.random.default_rng(43)
-    for n_rows in (9, 400, 2100):
+    for n_rows in (9, 400, 2100, 33000):
         x, ex, off_t, off = _case(rng, n_rows, 3, 256, 72, "bf16", True)
         wide = torch.full((n_rows, 264), 3.0, dtype=torch.bfloat16, device="cuda")
         wide[:, :256] = x
@@ -143,7 +146,7 @@ def test_strided_rows_and_outputs(moe):
         assert torch.equal(got, ref) and torch.all(buf[:, :3] == 5) and torch.all(buf[:, 259:] == 5)
 
 
-@pytest.mark.parametrize("n_rows", [5, 200, 2100])
+@pytest.mark.parametrize("n_rows", [5, 200, 2100, 33000])
 def test_non_finite_rows_stay_their_own(moe, n_rows):
     rng = np.random.default_rng(47)
     x, ex, off_t, off = _case(rng, n_rows, 2, 256, 64, "bf16", True)
@@ -157,10 +160,27 @@ def test_non_finite_rows_stay_their_own(moe, n_rows):
     assert torch.isnan(got[n_rows // 2]).all() and not torch.isfinite(got[0]).all()
 
 
+@pytest.mark.parametrize("n_rows", [5, 40, 60, 200, 33000])
+def test_non_finite_gradients_stay_their_own(moe, n_rows):
+    rng = np.random.default_rng(59)
+    dy, ex, off_t, off = _case(rng, n_rows, 2, 256, 70, "bf16", True, backward=True)
+    assert dy.stride(0) == 72  # what fills the pitch, and the next row, is not multiplied
+    ref = moe.awq_w4a16_grouped_gemm_backward(dy, *export_dev(*ex), off_t)
+    wide = torch.as_strided(dy, (n_rows, 72), (72, 1))
+    wide[:, 70:] = float("nan")
+    assert torch.equal(moe.awq_w4a16_grouped_gemm_backward(dy, *export_dev(*ex), off_t), ref)
+    dy[n_rows // 2, 69], dy[0, 7] = float("nan"), float("inf")
+    got = moe.awq_w4a16_grouped_gemm_backward(dy, *export_dev(*ex), off_t)
+    fine = torch.ones(n_rows, dtype=torch.bool)
+    fine[[0, n_rows // 2]] = False
+    assert torch.equal(got.cpu()[fine], ref.cpu()[fine])
+    assert torch.isnan(got[n_rows // 2]).all() and not torch.isfinite(got[0]).all()
+
+
 def test_no_rows_at_all_and_offsets_outside_the_rows(moe):
     """Offsets are the caller's to change: they are clamped to the rows and to ascend."""
     rng = np.random.default_rng(53)
-    for n_rows in (6, 300, 2100):
+    for n_rows in (6, 300, 2100, 33000):
         x, ex, off_t, off = _case(rng, n_rows, 4, 128, 32, "bf16", True)
         y = torch.full((n_rows, 32), 7.0, device="cuda")
         moe.awq_w4a16_grouped_gemm(x, *export_dev(*ex), torch.zeros_like(off_t), y=y)
