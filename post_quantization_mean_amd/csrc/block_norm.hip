@@ -68,7 +68,8 @@ struct Places {
 };
 
 // KEEP: the weights stay in registers and the next row is loaded ahead; otherwise (wide rows) neither, which
-// the registers would not hold.
+// the registers would not hold: weights and gate are loaded a chunk at a time. 1170 x 28672 bf16 57 us (4.7 TB/s; whole
+// rows of weights spilled, 92), 2048 x 16384 float32 104 (5.2; 125), 1170 x 28672 float32, which still spills, 245 (2.2).
 template <typename T, int ITEMS, int TMAX, bool KEEP>
 __global__ __launch_bounds__(TMAX) void block_norm_kernel(BlockNormArgs a, Mat res_out, Mat h) {
   constexpr int V = kVec<T>;
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(TMAX) void block_norm_kernel(BlockNormArgs a, Mat r
   auto load_row = [&](int64_t n, Raw<T, ITEMS>& ly, Raw<T, ITEMS>& lr, Raw<T, ITEMS>& lg) {
     if (block) ly.load(a.y.p, n * a.y.ld, at.p);
     lr.load(a.residual.p, n * a.residual.ld, at.p);
-    if (token_gate) lg.load(a.gate, n * a.ld_gate, at.p);
+    if (KEEP && token_gate) lg.load(a.gate, n * a.ld_gate, at.p);
   };
   load_row(row, y, r, gt);
   if (KEEP) {
@@ -116,13 +117,13 @@ __global__ __launch_bounds__(TMAX) void block_norm_kernel(BlockNormArgs a, Mat r
       rs *= rstd_of(s[0], d, a.eps);
       y.keep_packed();
     }
-    if (!KEEP) {
-      if (a.w_post) w1.load(a.w_post, 0, at.p);
-      if (a.gate && !token_gate) gt.load(a.gate, 0, at.p);
-    }
     float v[ITEMS][V], s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
+      if (!KEEP) {  // a chunk at a time: the registers do not hold the row and its weights
+        if (a.w_post) w1.u[i] = load_raw((const T*)a.w_post, at.p[i]);
+        if (a.gate) gt.u[i] = load_raw((const T*)a.gate + row * a.ld_gate, at.p[i]);
+      }
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         v[i][k] = fmaf(y.at(i, k) * rs * w1.at(i, k), gt.at(i, k), r.at(i, k));
@@ -133,9 +134,9 @@ __global__ __launch_bounds__(TMAX) void block_norm_kernel(BlockNormArgs a, Mat r
     if (h.p) {
       block_sum(s, red[1]);
       const float rs2 = rstd_of(s[0], d, a.eps);
-      if (!KEEP) w2.load(a.w_pre, 0, at.p);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
+        if (!KEEP) w2.u[i] = load_raw((const T*)a.w_pre, at.p[i]);
 #pragma unroll
         for (int k = 0; k < V; ++k) v[i][k] *= rs2 * w2.at(i, k);
         store_own((T*)h.p + row * h.ld, at.p[i], v[i]);
