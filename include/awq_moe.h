@@ -62,7 +62,7 @@ extern "C" {
  *             res_out are then NULL.
  *   residual  [n_tokens, ld_residual].
  *   w_post, w_pre  [d] of dtype.
- *   gate      [d] of dtype when ld_gate == 0, else [n_tokens, ld_gate].
+ *   gate      [d] of dtype when ld_gate == 0, else [n_tokens, ld_gate]. (Pitches of NULL matrices are not used.)
  *   res_out   [n_tokens, ld_res_out], receives r' (NULL: not wanted). May be residual or y.
  *   h         [n_tokens, ld_h]; NULL exactly when w_pre is. May be y or residual, not res_out.
  * eps >= 0. d up to AWQ_MAX_NORM_WIDTH. n_tokens == 0 returns AWQ_ERR_NO_TOKENS. */
