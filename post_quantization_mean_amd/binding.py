@@ -125,6 +125,30 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+def _tensors(v):
+    """The tensors in an argument or a result."""
+    if isinstance(v, torch.Tensor):
+        yield v
+    elif isinstance(v, (dict, list, tuple)):
+        for u in v.values() if isinstance(v, dict) else v:
+            yield from _tensors(u)
+
+
+def _on_stream(stream, fn, *args):
+    """fn(*args) with `stream` current. torch hands a buffer out anew in the order of the stream that was current when it was
+    allocated, so what a call allocates has to come from the stream that its work goes to: a workspace of another stream's
+    would be overwritten while the kernels still use it. The outputs are the caller's to use on the stream that was current."""
+    if any(t.device != stream.device for t in _tensors(args)):
+        raise ValueError(f"the stream is of {stream.device}, an operand is not")
+    current = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        res = fn(*args)
+    if current != stream:
+        for t in _tensors(res):
+            t.record_stream(current)
+    return res
+
+
 def _dev(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")

@@ -138,7 +138,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const void* ids, boo
   __syncthreads();
   walk(ids, ids64, w0, w1, n_experts, id_bits, cnt + wave * n_experts, [&](int slot, int id, int place) {
     position[slot] = id < n_experts ? place : -1;
-    if (id < n_experts && place < n_slots) order[place] = slot;
+    // (counts that a caller's other work has overwritten must not lead out of `order`)
+    if (id < n_experts && (unsigned)place < (unsigned)n_slots) order[place] = slot;
   });
   for (int i = max(b0, kept) + tid; i < b1; i += kSortThreads) order[i] = -1;
 }

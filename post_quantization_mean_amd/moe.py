@@ -1,8 +1,10 @@
 """Thin Python binding of the 4-bit mixture-of-experts block (include/awq_moe.h, in libawq_mi355x.so).
 
 As in `binding`, every function has the name of the C entry point it calls and only marshals arguments;
-outputs are allocated unless given. Work goes to torch's current stream of the tensors' device, or to
-`stream` (a stream of that device). The *_backward functions are the gradients; the quantized weights
+outputs are allocated unless given. Work goes to torch's current stream of the tensors' device. With `stream`
+(a stream of that device) a call does what it does inside `torch.cuda.stream(stream)`: outputs and workspaces
+are allocated there too, and what is passed has to be ready on that stream and to outlive its work; an output that
+is used on another stream has to wait for it. The *_backward functions are the gradients; the quantized weights
 and the input multipliers are constants.
 """
 from __future__ import annotations
@@ -12,7 +14,7 @@ import ctypes
 import torch
 
 from . import binding
-from .binding import AwqError, _HALF_BITS, _buf, _c_i64, _c_int, _c_size, _vp, _workspace  # noqa: F401
+from .binding import AwqError, _HALF_BITS, _buf, _c_i64, _c_int, _c_size, _on_stream, _vp, _workspace  # noqa: F401
 
 AWQ_MAX_EXPERTS = 1024
 AWQ_MAX_TOP_K = 64
@@ -73,14 +75,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _call(fn, dev, stream, *args) -> None:
-    """Enqueues on `stream`, or on the current stream of the tensors' device, with that device current."""
+def _call(fn, dev, *args) -> None:
+    """Enqueues on the current stream of the tensors' device, with that device current."""
     index = dev.index
     if index == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+            status = fn(*args, _raw_stream(index))
     if status:
         binding._check(status)
 
@@ -157,6 +159,8 @@ def awq_block_norm(y, residual: torch.Tensor, w_pre=None, w_post=None, gate=None
     """{"residual": r', "h": h} with r' = residual + res_scale * gate * norm(y) * w_post (without w_post: y
     itself; y None: r' = residual, not returned) and h = norm(r') * w_pre (only with w_pre). gate is a
     vector [d] or a matrix [n_tokens, d]. `out` may hold "residual" (also residual itself) and "h"."""
+    if stream is not None:
+        return _on_stream(stream, awq_block_norm, y, residual, w_pre, w_post, gate, res_scale, eps, out)
     lib = _load()
     t, n, d, dev, args = _norm_args(y, residual, w_pre, w_post, gate, res_scale, eps)
     out = out or {}
@@ -165,7 +169,7 @@ def awq_block_norm(y, residual: torch.Tensor, w_pre=None, w_post=None, gate=None
         res["residual"], po, ldo = _output(out.get("residual"), "residual (output)", (n, d), t, dev)
     if w_pre is not None:
         res["h"], ph, ldh = _output(out.get("h"), "h", (n, d), t, dev)
-    _call(lib.awq_block_norm, dev, stream, *args, po, ldo, ph, ldh)
+    _call(lib.awq_block_norm, dev, *args, po, ldo, ph, ldh)
     return res
 
 
@@ -179,6 +183,9 @@ def awq_block_norm_backward(y, residual: torch.Tensor, d_res_out, d_h, w_pre=Non
     """The gradients of awq_block_norm from those of its outputs (d_res_out may be None, d_h is None without
     w_pre): "d_residual", and where the input is there "d_y", "d_w_pre", "d_w_post" and "d_gate" (float32
     for vectors). `wanted` limits them to the names it holds."""
+    if stream is not None:
+        return _on_stream(stream, awq_block_norm_backward, y, residual, d_res_out, d_h, w_pre, w_post, gate, res_scale,
+                          eps, workspace, out, wanted)
     lib = _load()
     t, n, d, dev, args = _norm_args(y, residual, w_pre, w_post, gate, res_scale, eps)
     pr, ldr = (None, 0) if d_res_out is None else _matrix(d_res_out, "d_res_out", (n, d), t, dev)
@@ -201,7 +208,7 @@ def awq_block_norm_backward(y, residual: torch.Tensor, d_res_out, d_h, w_pre=Non
             o = torch.empty(d, dtype=torch.float32, device=dev) if o is None else o
             res[name], ptr[name] = o, (_vector(o, name, torch.float32, d, dev), 0)
     workspace = _workspace(lib.awq_block_norm_backward_workspace_bytes(n, d), dev, workspace)
-    _call(lib.awq_block_norm_backward, dev, stream, *args, pr, ldr, ph, ldh, *ptr["d_y"], *ptr["d_residual"],
+    _call(lib.awq_block_norm_backward, dev, *args, pr, ldr, ph, ldh, *ptr["d_y"], *ptr["d_residual"],
           ptr["d_w_post"][0], ptr["d_w_pre"][0], *ptr["d_gate"], workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
     return res
@@ -228,6 +235,8 @@ def awq_moe_sort_workspace_bytes(n_tokens: int, top_k: int, n_experts: int) -> i
 def awq_moe_sort(expert_ids: torch.Tensor, n_experts: int, workspace=None, out=None, stream=None) -> dict:
     """The stable order by expert of the slots of expert_ids ([n_tokens, top_k] int32 or int64; ids outside
     [0, n_experts) are dropped): int32 "offsets" [n_experts + 1], "order" [slots], "position" [n_tokens, top_k]."""
+    if stream is not None:
+        return _on_stream(stream, awq_moe_sort, expert_ids, n_experts, workspace, out)
     lib = _load()
     pi = _slots(expert_ids, "expert_ids", (torch.int32, torch.int64))
     n, k = expert_ids.shape
@@ -248,7 +257,7 @@ def awq_moe_sort(expert_ids: torch.Tensor, n_experts: int, workspace=None, out=N
     if nb:
         workspace = _workspace(nb, dev, workspace)
         pw, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(lib.awq_moe_sort, dev, stream, pi, expert_ids.element_size(), n, k, n_experts, *ptrs, pw, nb)
+    _call(lib.awq_moe_sort, dev, pi, expert_ids.element_size(), n, k, n_experts, *ptrs, pw, nb)
     return res
 
 
@@ -270,6 +279,8 @@ def awq_moe_gather(x: torch.Tensor, position: torch.Tensor, expert_ids=None, in_
     """rows [n_rows, d] with rows[position[t, j]] = x[t] * in_scales[expert_ids[t, j]] (in_scales: float32
     [n_experts, d], usually 1 / the scales searched for each expert). n_rows is the slots' count unless given,
     or that of `out`; rows that no slot names are left as they were."""
+    if stream is not None:
+        return _on_stream(stream, awq_moe_gather, x, position, expert_ids, in_scales, n_rows, out)
     lib = _load()
     dt = _data_dtype(x, "x")
     px, ldx = _matrix(x, "x")
@@ -281,13 +292,15 @@ def awq_moe_gather(x: torch.Tensor, position: torch.Tensor, expert_ids=None, in_
     if n_rows is None:
         n_rows = n * k if out is None else out.shape[0]
     rows, po, ldo = _output(out, "rows", (n_rows, d), x.dtype, dev)
-    _call(lib.awq_moe_gather, dev, stream, px, ldx, dt, n, d, pp, k, *ids, po, ldo, n_rows)
+    _call(lib.awq_moe_gather, dev, px, ldx, dt, n, d, pp, k, *ids, po, ldo, n_rows)
     return rows
 
 
 def awq_moe_gather_backward(d_rows: torch.Tensor, position: torch.Tensor, expert_ids=None, in_scales=None, out=None,
                             stream=None) -> torch.Tensor:
     """d_x [n_tokens, d]: the sum of each token's rows of d_rows, times in_scales."""
+    if stream is not None:
+        return _on_stream(stream, awq_moe_gather_backward, d_rows, position, expert_ids, in_scales, out)
     lib = _load()
     dt = _data_dtype(d_rows, "d_rows")
     pr, ldr = _matrix(d_rows, "d_rows")
@@ -297,13 +310,15 @@ def awq_moe_gather_backward(d_rows: torch.Tensor, position: torch.Tensor, expert
     n, k = position.shape
     ids = _scale_args(in_scales, expert_ids, n, k, d, dev)
     d_x, po, ldo = _output(out, "d_x", (n, d), d_rows.dtype, dev)
-    _call(lib.awq_moe_gather_backward, dev, stream, pr, ldr, dt, n_rows, d, pp, n, k, *ids, po, ldo)
+    _call(lib.awq_moe_gather_backward, dev, pr, ldr, dt, n_rows, d, pp, n, k, *ids, po, ldo)
     return d_x
 
 
 def awq_moe_combine(rows: torch.Tensor, position: torch.Tensor, weights: torch.Tensor, out=None,
                     stream=None) -> torch.Tensor:
     """out [n_tokens, d]: the sum over j of weights[t, j] (float32) * rows[position[t, j]]."""
+    if stream is not None:
+        return _on_stream(stream, awq_moe_combine, rows, position, weights, out)
     lib = _load()
     dt = _data_dtype(rows, "rows")
     pr, ldr = _matrix(rows, "rows")
@@ -313,7 +328,7 @@ def awq_moe_combine(rows: torch.Tensor, position: torch.Tensor, weights: torch.T
     n, k = position.shape
     pw = _slots(weights, "weights", torch.float32, n, k, dev)
     res, po, ldo = _output(out, "out", (n, d), rows.dtype, dev)
-    _call(lib.awq_moe_combine, dev, stream, pr, ldr, dt, n_rows, d, pp, pw, n, k, po, ldo)
+    _call(lib.awq_moe_combine, dev, pr, ldr, dt, n_rows, d, pp, pw, n, k, po, ldo)
     return res
 
 
@@ -321,6 +336,8 @@ def awq_moe_combine_backward(d_out: torch.Tensor, rows: torch.Tensor, position: 
                              out=None, stream=None) -> dict:
     """{"d_rows": weights[t, j] * d_out[t] at position[t, j], "d_weights": <d_out[t], rows[position[t, j]]>}.
     `out` may hold either; rows of d_rows that no slot names are left as they were."""
+    if stream is not None:
+        return _on_stream(stream, awq_moe_combine_backward, d_out, rows, position, weights, out)
     lib = _load()
     dt = _data_dtype(rows, "rows")
     pr, ldr = _matrix(rows, "rows")
@@ -336,7 +353,7 @@ def awq_moe_combine_backward(d_out: torch.Tensor, rows: torch.Tensor, position: 
     if d_weights is None:
         d_weights = torch.empty(n, k, dtype=torch.float32, device=dev)
     pdw = _slots(d_weights, "d_weights", torch.float32, n, k, dev)
-    _call(lib.awq_moe_combine_backward, dev, stream, pd, ldd, pr, ldr, dt, n_rows, d, pp, pw, n, k, po, ldo, pdw)
+    _call(lib.awq_moe_combine_backward, dev, pd, ldd, pr, ldr, dt, n_rows, d, pp, pw, n, k, po, ldo, pdw)
     return {"d_rows": d_rows, "d_weights": d_weights}
 
 
@@ -379,6 +396,8 @@ def awq_w4a16_grouped_gemm(x: torch.Tensor, codes: torch.Tensor, steps_f16: torc
     [n_experts, d_out, d_in/128], zeros_u4 [n_experts, d_out, ceil(d_in/256)]). act "silu" or "relu": the
     weights stack a gate and an up matrix, and y = act(x gate^T) * (x up^T). y is x's dtype or float32; rows from
     offsets[n_experts] on are left as they were."""
+    if stream is not None:
+        return _on_stream(stream, awq_w4a16_grouped_gemm, x, codes, steps_f16, zeros_u4, offsets, act, out_dtype, y)
     lib = _load()
     if act not in _MODES:
         raise ValueError(f"act {act!r} is none of None, 'silu', 'relu'")
@@ -388,7 +407,7 @@ def awq_w4a16_grouped_gemm(x: torch.Tensor, codes: torch.Tensor, steps_f16: torc
     if act is not None and d_out % 2:
         raise ValueError(f"d_out {d_out} of a gate/up pair is odd")
     y, py, ldy, yd = _grouped_output(x, y, "y", (n, d_out if act is None else d_out // 2), out_dtype)
-    _call(lib.awq_w4a16_grouped_gemm, x.device, stream, px, ldx, _DTYPES[x.dtype], *ptrs, e, n, d_in, d_out, _MODES[act],
+    _call(lib.awq_w4a16_grouped_gemm, x.device, px, ldx, _DTYPES[x.dtype], *ptrs, e, n, d_in, d_out, _MODES[act],
           py, ldy, yd)
     return y
 
@@ -398,11 +417,14 @@ def awq_w4a16_grouped_gemm_backward(d_y: torch.Tensor, codes: torch.Tensor, step
                                     stream=None) -> torch.Tensor:
     """d_x [n_rows, d_in]: row i of d_y ([n_rows, d_out]) times its expert's dequantized weights, not
     transposed: the gradient of the plain product with respect to x."""
+    if stream is not None:
+        return _on_stream(stream, awq_w4a16_grouped_gemm_backward, d_y, codes, steps_f16, zeros_u4, offsets, out_dtype,
+                          dx)
     lib = _load()
     ptrs, e, d_in, d_out = _export_args(d_y, codes, steps_f16, zeros_u4, offsets)
     pd, ldd = _matrix(d_y, "d_y", (d_y.shape[0], d_out) if d_y.dim() == 2 else None)
     n = d_y.shape[0]
     dx, px, ldx, xd = _grouped_output(d_y, dx, "dx", (n, d_in), out_dtype)
-    _call(lib.awq_w4a16_grouped_gemm_backward, d_y.device, stream, pd, ldd, _DTYPES[d_y.dtype], *ptrs, e, n, d_in, d_out,
+    _call(lib.awq_w4a16_grouped_gemm_backward, d_y.device, pd, ldd, _DTYPES[d_y.dtype], *ptrs, e, n, d_in, d_out,
           px, ldx, xd)
     return dx
