@@ -3,11 +3,15 @@
 Every function has the name of the C entry point it calls and only marshals arguments:
 torch supplies device memory (tensors, workspaces) and the stream; every step of the
 computation runs in the library's HIP kernels. If the library is missing the functions
-raise instead of computing anything another way.
+raise instead of computing anything another way. With `stream` a call does what it does inside
+`torch.cuda.stream(stream)`: what it allocates belongs to that stream, and what is passed has to be
+ready on it and to outlive its work.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -149,6 +153,21 @@ def _on_stream(stream, fn, *args):
     return res
 
 
+def _streamed(fn):
+    """fn, whose last argument is `stream`, run on it (_on_stream)."""
+    at = len(inspect.signature(fn).parameters) - 1
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        kw.pop("stream", None)
+        return _on_stream(stream, lambda a, k: fn(*a, **k), args[:at], kw)
+
+    return call
+
+
 def _dev(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -227,6 +246,7 @@ def awq_act_stats_workspace_bytes(dtype: int, n_tokens: int, d_in: int) -> int:
     return load_library().awq_act_stats_workspace_bytes(dtype, n_tokens, d_in)
 
 
+@_streamed
 def awq_act_stats(x: torch.Tensor, act_mean: torch.Tensor | None = None, workspace=None, stream=None):
     """a1: float64 [d_in] mean of |x| over tokens."""
     lib = load_library()
@@ -241,6 +261,7 @@ def awq_act_stats(x: torch.Tensor, act_mean: torch.Tensor | None = None, workspa
     return act_mean
 
 
+@_streamed
 def awq_candidate_scales(act_mean: torch.Tensor, n_grid: int, cand_scales=None, stream=None):
     """a2: float64 [n_grid, d_in] candidate scales."""
     lib = load_library()
@@ -253,6 +274,7 @@ def awq_candidate_scales(act_mean: torch.Tensor, n_grid: int, cand_scales=None, 
     return cand_scales
 
 
+@_streamed
 def awq_quant_delta(w_parts, cand_scales: torch.Tensor, group_size: int = GROUP_SIZE, delta=None, stream=None):
     """a3: [n_cand, d_out, d_in] delta = What - W in the weights' dtype."""
     lib = load_library()
@@ -278,6 +300,7 @@ def awq_error_tiles(n_tokens: int, d_out: int) -> int:
     return load_library().awq_error_tiles(n_tokens, d_out)
 
 
+@_streamed
 def awq_error_sse(x: torch.Tensor, delta: torch.Tensor, tile_sse=None, stream=None):
     """a4: float64 [n_cand, tiles] per-tile sums of squares of x @ delta_j^T."""
     lib = load_library()
@@ -308,6 +331,7 @@ def awq_gram_workspace_bytes(n_tokens: int, d_in: int) -> int:
     return load_library().awq_gram_workspace_bytes(n_tokens, d_in)
 
 
+@_streamed
 def awq_gram(x: torch.Tensor, gram=None, gram_exp=None, workspace=None, stream=None):
     """G = X^T X of bfloat16 activations as (float16 [d_in, d_in] holding G * 2^e, int32 [1] = e)."""
     lib = load_library()
@@ -324,6 +348,7 @@ def awq_gram(x: torch.Tensor, gram=None, gram_exp=None, workspace=None, stream=N
     return gram, gram_exp
 
 
+@_streamed
 def awq_quant_delta_f16(w_parts, cand_scales: torch.Tensor, group_size: int = GROUP_SIZE, delta=None,
                         delta_exp=None, stream=None):
     """a3 for the Gram form: (float16 [n_cand, d_out, d_in] holding delta * 2^e_k, int32 [n_cand + 1]
@@ -341,6 +366,7 @@ def awq_quant_delta_f16(w_parts, cand_scales: torch.Tensor, group_size: int = GR
     return delta, delta_exp
 
 
+@_streamed
 def awq_gram_error_sse(gram: torch.Tensor, gram_exp: torch.Tensor, delta: torch.Tensor, delta_exp: torch.Tensor,
                        n_tokens: int, tile_sse=None, stream=None):
     """a4 in the Gram form: float64 [n_cand, awq_error_tiles(n_tokens, d_out)] tile shares of each
@@ -363,6 +389,7 @@ def awq_gram_error_sse(gram: torch.Tensor, gram_exp: torch.Tensor, delta: torch.
     return tile_sse
 
 
+@_streamed
 def awq_loss_argmin(tile_sse: torch.Tensor, n_tokens: int, d_out: int, cand_scales: torch.Tensor,
                     losses=None, best_scales=None, best_info=None, stream=None):
     """a5: (losses [n_grid] f64, best_scales [d_in] f64, best_info [2] i32 = {k*, flags})."""
@@ -410,6 +437,7 @@ def awq_search_workspace_bytes(dtype: int, n_tokens: int, d_in: int, d_out: int,
                                                      cand_per_pass)
 
 
+@_streamed
 def awq_search_scales(x: torch.Tensor, w_parts, act_mean: torch.Tensor, n_grid: int = 20,
                       group_size: int = GROUP_SIZE, cand_per_pass: int | None = None, workspace=None,
                       out=None, stream=None) -> dict:
@@ -432,6 +460,7 @@ def awq_search_scales(x: torch.Tensor, w_parts, act_mean: torch.Tensor, n_grid: 
     return res
 
 
+@_streamed
 def awq_search_scales_noalloc(x: torch.Tensor, w_parts, act_mean: torch.Tensor, n_grid: int = 20,
                               group_size: int = GROUP_SIZE, out=None, stream=None) -> dict:
     """awq_search_scales with the library's fixed device scratch instead of a workspace: the C call
@@ -450,6 +479,7 @@ def awq_search_scales_noalloc(x: torch.Tensor, w_parts, act_mean: torch.Tensor, 
     return res
 
 
+@_streamed
 def awq_quantize_pack(w_parts, s: torch.Tensor, group_size: int = GROUP_SIZE, out=None, stream=None) -> dict:
     """a6: codes [d_out, d_in/2] u8, qscales [d_out, d_in/128] f32, zeros [d_out, d_in/128] i32."""
     lib = load_library()
@@ -475,6 +505,7 @@ def awq_quantize_pack(w_parts, s: torch.Tensor, group_size: int = GROUP_SIZE, ou
     return {"codes": codes, "qscales": qs, "zeros": zs}
 
 
+@_streamed
 def awq_act_stats_accumulate(x: torch.Tensor, sums: torch.Tensor, workspace=None, stream=None):
     """sums (float64 [d_in], device) += per-channel sum of |x| over this batch's tokens."""
     lib = load_library()
@@ -487,6 +518,7 @@ def awq_act_stats_accumulate(x: torch.Tensor, sums: torch.Tensor, workspace=None
     return sums
 
 
+@_streamed
 def awq_act_stats_finalize(sums: torch.Tensor, total_tokens: int, act_mean=None, stream=None):
     """act_mean = sums / total_tokens (float64 [d_in])."""
     lib = load_library()
@@ -499,6 +531,7 @@ def awq_act_stats_finalize(sums: torch.Tensor, total_tokens: int, act_mean=None,
     return act_mean
 
 
+@_streamed
 def awq_fold_scales(src: torch.Tensor, s: torch.Tensor, dst=None, stream=None):
     """Row r of src ([rows] or [rows, cols], bf16 or f32) divided by s[r] (float64 [rows])."""
     lib = load_library()
@@ -517,6 +550,7 @@ def awq_fold_scales(src: torch.Tensor, s: torch.Tensor, dst=None, stream=None):
     return dst
 
 
+@_streamed
 def awq_tie_heads(act_mean: torch.Tensor, n_heads: int, n_kv_heads: int, head_dim: int, out=None, stream=None):
     """Statistic of the o_proj input channels tied across the query heads that share a KV head
     (float64 [n_heads * head_dim]); `out` may be act_mean."""
@@ -530,6 +564,7 @@ def awq_tie_heads(act_mean: torch.Tensor, n_heads: int, n_kv_heads: int, head_di
     return out
 
 
+@_streamed
 def awq_head_group_scales(s: torch.Tensor, n_heads: int, n_kv_heads: int, head_dim: int, out=None, stream=None):
     """The v_proj row scales (float64 [n_kv_heads * head_dim]) of tied o_proj scales s."""
     lib = load_library()
@@ -542,6 +577,7 @@ def awq_head_group_scales(s: torch.Tensor, n_heads: int, n_kv_heads: int, head_d
     return out
 
 
+@_streamed
 def awq_export_fp16(qscales: torch.Tensor, zeros: torch.Tensor, out=None, stream=None) -> dict:
     """Float16 steps (uint16 bits) and zero points packed two per byte, with the two counts."""
     lib = load_library()
@@ -575,6 +611,7 @@ def _ratios(ratios):
 _HALF_BITS = (torch.int16, torch.uint16, torch.float16)  # 16-bit containers of float16 bits
 
 
+@_streamed
 def awq_weight_mean(w_parts, w_mean=None, workspace=None, stream=None):
     """float64 [d_in] mean of |W| over the stacked output rows of the parts."""
     lib = load_library()
@@ -592,6 +629,7 @@ def awq_weight_mean(w_parts, w_mean=None, workspace=None, stream=None):
     return w_mean
 
 
+@_streamed
 def awq_candidate_scales_ex(act_mean: torch.Tensor, ratios, formula: int = AWQ_FORMULA_MSMODELSLIM,
                             w_mean=None, cand_scales=None, stream=None):
     """float64 [len(ratios), d_in] candidate scales of a formula over an explicit ratio list."""
@@ -608,6 +646,7 @@ def awq_candidate_scales_ex(act_mean: torch.Tensor, ratios, formula: int = AWQ_F
     return cand_scales
 
 
+@_streamed
 def awq_quant_delta_ex(w_parts, cand_scales: torch.Tensor, quantizer: int = AWQ_QUANT_INT4_GROUP, delta=None,
                        stream=None):
     """[n_cand, d_out, d_in] delta = What - W under the chosen quantizer, in the weights' dtype."""
@@ -623,6 +662,7 @@ def awq_quant_delta_ex(w_parts, cand_scales: torch.Tensor, quantizer: int = AWQ_
     return delta
 
 
+@_streamed
 def awq_search_scales_ex(x: torch.Tensor, w_parts, act_mean: torch.Tensor, ratios,
                          formula: int = AWQ_FORMULA_MSMODELSLIM, quantizer: int = AWQ_QUANT_INT4_GROUP,
                          w_mean=None, cand_per_pass: int | None = None, workspace=None, out=None,
@@ -649,6 +689,7 @@ def awq_search_scales_ex(x: torch.Tensor, w_parts, act_mean: torch.Tensor, ratio
     return res
 
 
+@_streamed
 def awq_w4a16_gemm(x: torch.Tensor, codes: torch.Tensor, steps_f16: torch.Tensor, zeros_u4: torch.Tensor,
                    out_dtype=torch.float32, y=None, stream=None):
     """Y [n_tokens, d_out] = x @ W_hat^T, W_hat dequantized on the fly from the deployment form
@@ -697,6 +738,7 @@ def _x_bf16(x: torch.Tensor):
     return _x_args(x)
 
 
+@_streamed
 def awq_mlp_hidden_ref(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, g_ref=None, u_ref=None,
                        stream=None):
     """(g_ref, u_ref) = (x @ w_gate^T, x @ w_up^T) in float32, [n_tokens, d_ff] each."""
@@ -715,6 +757,7 @@ def awq_mlp_hidden_ref(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor
     return g_ref, u_ref
 
 
+@_streamed
 def awq_mlp_hidden_delta(x: torch.Tensor, dw_gate: torch.Tensor, dw_up: torch.Tensor, g_ref: torch.Tensor,
                          u_ref: torch.Tensor, act: int = AWQ_ACT_SILU, dh=None, stream=None):
     """dh = act(g) u - act(g + x dw_gate^T)(u + x dw_up^T), bfloat16 [n_tokens, d_ff]."""
@@ -738,6 +781,7 @@ def awq_search_workspace_bytes_mlp(n_tokens: int, d_in: int, d_ff: int, d_model:
     return load_library().awq_search_workspace_bytes_mlp(n_tokens, d_in, d_ff, d_model, n_grid, cand_per_pass)
 
 
+@_streamed
 def awq_search_scales_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                           act_mean: torch.Tensor, act: int = AWQ_ACT_SILU, n_grid: int = 20,
                           cand_per_pass: int | None = None, workspace=None, out=None, stream=None) -> dict:
@@ -764,6 +808,7 @@ def awq_search_scales_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Ten
     return res
 
 
+@_streamed
 def awq_layer(x: torch.Tensor, w_parts, n_grid: int = 20, group_size: int = GROUP_SIZE,
               cand_per_pass: int | None = None, stream=None) -> dict:
     """The whole hot path for one layer: statistic, search, final quantize + pack."""

@@ -75,6 +75,13 @@ def test_a_call_of_the_experts_block_allocates_on_its_stream(monkeypatch, stream
     assert at == [[s]]
 
 
+@pytest.mark.parametrize("positional", [False, True])
+@pytest.mark.parametrize("f", _functions(binding), ids=lambda f: f.__name__)
+def test_a_call_of_the_search_allocates_on_its_stream(monkeypatch, streams, f, positional):
+    at, s = _library_asked_for(monkeypatch, binding, "load_library", f, streams[1], positional)
+    assert at == [[s]]
+
+
 def test_outputs_are_recorded_on_the_stream_that_was_current(streams):
     current, inside = streams
     made = [torch.zeros(2).as_subclass(_Tensor) for _ in range(3)]
