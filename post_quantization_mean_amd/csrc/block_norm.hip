@@ -81,10 +81,10 @@ __global__ __launch_bounds__(TMAX) void block_norm_kernel(BlockNormArgs a, Mat r
   Raw<T, ITEMS> w1, w2, gt, y, r, yn, rn, gn;
   w1.fill(raw_ones<T>());
   gt.fill(raw_ones<T>());
-  y.fill(make_uint4(0, 0, 0, 0));
   int64_t row = blockIdx.x;
   auto load_row = [&](int64_t n, Raw<T, ITEMS>& ly, Raw<T, ITEMS>& lr, Raw<T, ITEMS>& lg) {
     if (block) ly.load(a.y.p, n * a.y.ld, at.p);
+    else ly.fill(make_uint4(0, 0, 0, 0));  // in every row: the row ahead has registers of its own
     lr.load(a.residual.p, n * a.residual.ld, at.p);
     if (KEEP && token_gate) lg.load(a.gate, n * a.ld_gate, at.p);
   };

@@ -145,3 +145,15 @@ def test_several_rows_in_place(moe, n, d, dtype):
                                       **args)
     for name in back:
         assert torch.equal(got[name], back[name]), name
+
+
+@pytest.mark.parametrize("n,d,dtype", [(4500, 257, "bf16"), (2100, 520, "bf16"), (1200, 4096, "bf16"), (1200, 4096, "f32"),
+                                       (600, 11008, "f16"), (300, 28672, "bf16")])
+def test_the_first_norm_of_a_model_takes_several_rows(moe, n, d, dtype):
+    """Without y every row's r' is its residual, the rows behind a block's first one too."""
+    print(f"[gpu norm rows] first norm n={n} d={d} {dtype}", flush=True)
+    v, g = inputs(n, n, d, dtype, None, post=False, block=False)
+    got = moe.awq_block_norm(None, v["residual"], v["w_pre"], eps=EPS)
+    check(got, *reference(v, None, 1.0), dtype)
+    got = moe.awq_block_norm_backward(None, v["residual"], g["d_res"], g["d_h"], v["w_pre"], eps=EPS)
+    check(got, *reference(v, g, 1.0), dtype)
