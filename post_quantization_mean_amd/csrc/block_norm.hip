@@ -93,13 +93,18 @@ __global__ __launch_bounds__(TMAX) void block_norm_kernel(BlockNormArgs a, Mat r
     if (a.w_post) w1.load(a.w_post, 0, at.p);
     if (a.gate && !token_gate) gt.load(a.gate, 0, at.p);
     if (a.w_pre) w2.load(a.w_pre, 0, at.p);
+    if (ragged) {  // zero where a lane owns nothing, as y and r: the sum does not see the neighbours' infinities
+      w1.own(at.p);
+      gt.own(at.p);
+    }
   }
   for (; row < a.n; row += gridDim.x) {
     const int64_t next = row + gridDim.x;
     if (KEEP && next < a.n) load_row(next, yn, rn, gn);
     if (ragged) {
       y.own(at.p);
-      r.own(at.p);
+      if (KEEP) r.own(at.p);
+      if (KEEP && token_gate) gt.own(at.p);
     }
     if (KEEP) {
       w1.keep_packed();
@@ -127,6 +132,8 @@ __global__ __launch_bounds__(TMAX) void block_norm_kernel(BlockNormArgs a, Mat r
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         v[i][k] = fmaf(y.at(i, k) * rs * w1.at(i, k), gt.at(i, k), r.at(i, k));
+        // only a last chunk can be cut: a block has more threads than chunks too many
+        if (!KEEP && i == ITEMS - 1) v[i][k] = k < at.p[i].skip ? 0.f : v[i][k];
         s[0] = fmaf(v[i][k], v[i][k], s[0]);
       }
       if (res_out.p) store_own((T*)res_out.p + row * res_out.ld, at.p[i], v[i]);
@@ -230,6 +237,11 @@ __global__ __launch_bounds__(512) void block_norm_backward_kernel(BlockNormArgs 
   if (a.w_post) w1.load(a.w_post, 0, at.p);
   if (a.w_pre) w2.load(a.w_pre, 0, at.p);
   if (!TOKEN && a.gate) wg.load(a.gate, 0, at.p);
+  if (ragged) {  // zero of every input where a lane owns nothing: the sums do not see the neighbours' weights
+    w1.own(at.p);
+    w2.own(at.p);
+    wg.own(at.p);
+  }
   for (; row < a.n; row += gridDim.x) {
     const int64_t next = row + gridDim.x;
     if (AHEAD && next < a.n) load_into(next, ahead, ahead.y);
@@ -238,6 +250,7 @@ __global__ __launch_bounds__(512) void block_norm_backward_kernel(BlockNormArgs 
       c.r.own(at.p);
       c.dr.own(at.p);
       c.dh.own(at.p);
+      if (TOKEN) c.gt.own(at.p);
     }
     auto keep_packed = [&]() {
       w1.keep_packed();

@@ -1,0 +1,80 @@
+"""Infinities and NaN in the inputs of awq_block_norm and its gradient: NaN, infinities and finite values lie where the
+formulas put them in float64. The finite values that are left beside them are products of zero."""
+import numpy as np
+import pytest
+
+from oracle import awq_moe as M
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from moe_cases import dev, host, within  # noqa: E402
+
+EPS = 2.0 ** -20
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from post_quantization_mean_amd import moe
+    moe._load()
+    return moe
+
+
+def _make(seed, n, d, dtype, **parts):
+    """Values away from zero (0 * inf would be another pattern); parts: names with the changes {element: value}."""
+    rng = np.random.default_rng(seed)
+    mk = lambda *s: rng.choice([-1.0, 1.0], s) * rng.uniform(0.25, 2.0, s)  # noqa: E731
+    v = {"y": mk(n, d), "residual": mk(n, d), "w_pre": mk(d), "w_post": mk(d), "gate": mk(d), "d_res": mk(n, d), "d_h": mk(n, d)}
+    for name, change in parts.items():
+        if change is None:
+            v[name] = None
+            continue
+        if name == "gate" and change.get("token"):
+            v[name] = mk(n, d)
+        for at, value in change.items():
+            if at != "token":
+                v[name][..., at] = value
+    t = {k: None if a is None else dev(a, dtype) for k, a in v.items()}
+    return t, {k: None if a is None else host(a) for k, a in t.items()}
+
+
+def _forward(moe, t, v, a, dtype):
+    got = moe.awq_block_norm(t["y"], t["residual"], t["w_pre"], t["w_post"], t["gate"], a, EPS)
+    with np.errstate(invalid="ignore"):
+        want = dict(zip(("residual", "h"), M.block_norm(v["y"], v["residual"], v["w_pre"], v["w_post"], v["gate"], a, EPS)))
+    return got, want
+
+
+def _backward(moe, t, v, a, wanted):
+    got = moe.awq_block_norm_backward(t["y"], t["residual"], t["d_res"], t["d_h"], t["w_pre"], t["w_post"], t["gate"], a, EPS,
+                                      wanted=wanted)
+    with np.errstate(invalid="ignore"):
+        want = M.block_norm_backward(v["y"], v["residual"], v["w_pre"], v["w_post"], v["gate"], a, EPS, v["d_res"], v["d_h"])
+    return got, want
+
+
+# widths that leave lanes of a block without whole chunks, registers and wide rows; an element of the row's end, and one of
+# the chunk before it that the moved-back last chunk covers too
+RAGGED = [(3, 257, "bf16", 256), (2, 520, "bf16", 519), (3, 1037, "bf16", 1030), (3, 1037, "bf16", 1036), (2, 4100, "f32", 4099),
+          (2, 4099, "f16", 4093), (2, 20000, "bf16", 19999), (1, 28670, "f32", 28666)]
+
+
+@pytest.mark.parametrize("name,token", [("gate", False), ("gate", True), ("w_post", False)])
+@pytest.mark.parametrize("n,d,dtype,at", RAGGED)
+def test_infinite_weights_at_the_end_of_ragged_rows(moe, n, d, dtype, at, name, token):
+    """One infinity in r' makes its norm infinite: h is 0 wherever r' is finite, and NaN where it is not."""
+    t, v = _make(d, n, d, dtype, **{name: {at: INF, "token": token} if token else {at: INF}})
+    got, want = _forward(moe, t, v, 0.5, dtype)
+    assert np.isnan(want["h"]).sum() == n and np.all(np.delete(want["h"], at, 1) == 0)
+    within(host(got["h"]), want["h"], 0.0, "h")
+
+
+@pytest.mark.parametrize("n,d,dtype,at", [c for c in RAGGED if c[1] <= 8192])
+def test_gradients_of_an_infinite_norm_weight_at_the_end_of_ragged_rows(moe, n, d, dtype, at):
+    t, v = _make(d, n, d, dtype, w_pre={at: INF})
+    got, want = _backward(moe, t, v, 0.5, ["d_residual"])
+    assert np.isinf(want["d_residual"]).sum() == n * (d - 1)
+    within(host(got["d_residual"]), want["d_residual"], 0.0, "d_residual")
