@@ -1,5 +1,6 @@
 """Infinities and NaN in the inputs of awq_block_norm and its gradient: NaN, infinities and finite values lie where the
-formulas put them in float64. The finite values that are left beside them are products of zero."""
+formulas put them in float64. The finite values that are left beside them are products of zero, copies, or one product of
+three factors (3 U and a rounding), U = 2^-24."""
 import numpy as np
 import pytest
 
@@ -8,7 +9,7 @@ from oracle import awq_moe as M
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from moe_cases import dev, host, within  # noqa: E402
+from moe_cases import U, dev, half_step, host, within  # noqa: E402
 
 EPS = 2.0 ** -20
 INF = float("inf")
@@ -72,9 +73,43 @@ def test_infinite_weights_at_the_end_of_ragged_rows(moe, n, d, dtype, at, name, 
     within(host(got["h"]), want["h"], 0.0, "h")
 
 
+@pytest.mark.parametrize("name", ["gate", "w_post"])
+@pytest.mark.parametrize("n,d,dtype,at", [c for c in RAGGED if c[1] <= 8192])
+def test_gradients_of_infinite_weights_at_the_end_of_ragged_rows(moe, n, d, dtype, at, name):
+    """Without a norm behind the residual: t is infinite in one element, and d_y = (t - u mean(t u)) / n1 in all."""
+    t, v = _make(d, n, d, dtype, w_pre=None, d_h=None, **{name: {at: INF}})
+    got, want = _backward(moe, t, v, 0.5, ["d_y"])
+    assert np.isinf(want["d_y"]).sum() == n * (d - 1)
+    within(host(got["d_y"]), want["d_y"], 0.0, "d_y")
+
+
 @pytest.mark.parametrize("n,d,dtype,at", [c for c in RAGGED if c[1] <= 8192])
 def test_gradients_of_an_infinite_norm_weight_at_the_end_of_ragged_rows(moe, n, d, dtype, at):
     t, v = _make(d, n, d, dtype, w_pre={at: INF})
     got, want = _backward(moe, t, v, 0.5, ["d_residual"])
     assert np.isinf(want["d_residual"]).sum() == n * (d - 1)
     within(host(got["d_residual"]), want["d_residual"], 0.0, "d_residual")
+
+
+# registers, strips of columns, rows narrower than a chunk
+@pytest.mark.parametrize("bad", [INF, float("nan")])
+@pytest.mark.parametrize("name", ["residual", "y", "w_post", "gate"])
+@pytest.mark.parametrize("d", [5, 520, 4096, 9003])
+def test_a_gradient_that_does_not_pass_the_norm_does_not_see_its_input(moe, d, name, bad):
+    """Without a norm behind it, d_residual is d_res_out whatever r' holds."""
+    t, v = _make(d, 3, d, "bf16", w_pre=None, d_h=None, **{name: {d // 2: bad}})
+    got, want = _backward(moe, t, v, 0.5, ["d_residual"])
+    assert np.array_equal(host(got["d_residual"]), v["d_res"]) and np.array_equal(want["d_residual"], v["d_res"])
+
+
+@pytest.mark.parametrize("bad", [INF, float("nan")])
+@pytest.mark.parametrize("d", [5, 520, 4096, 9003])
+def test_the_gradient_of_a_block_without_a_norm_does_not_see_its_output(moe, d, bad):
+    """r' = residual + a gate y, without norms: d_y = a gate d_res_out, whatever y holds; d_gate has y in it."""
+    t, v = _make(d, 3, d, "bf16", w_pre=None, w_post=None, d_h=None, y={d // 2: bad})
+    got, want = _backward(moe, t, v, 0.5, ["d_y", "d_residual", "d_gate"])
+    assert np.isfinite(want["d_y"]).all()
+    hs = half_step("bf16")
+    for k in ("d_y", "d_residual"):
+        within(host(got[k]), want[k], (3 * U * (1 + hs) + hs) * np.abs(want[k]), k)
+    within(host(got["d_gate"]), want["d_gate"], 6 * U * 3 * 4, "d_gate")  # three terms of at most a d_res y = 2
