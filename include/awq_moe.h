@@ -59,7 +59,7 @@ extern "C" {
  * y is the output of the block just run, h the input of the next one; w_pre is usually a norm weight that
  * awq_fold_scales has divided by the next linear's scales.
  *   y         [n_tokens, ld_y], or NULL: r' = residual (the first norm of a model); w_post, gate and
- *             res_out are then NULL.
+ *             res_out are then NULL, and res_scale is not used.
  *   residual  [n_tokens, ld_residual].
  *   w_post, w_pre  [d] of dtype.
  *   gate      [d] of dtype when ld_gate == 0, else [n_tokens, ld_gate]. (Pitches of NULL matrices are not used.)

@@ -76,9 +76,10 @@ int check_norm(const void* y, int64_t ld_y, const void* residual, int64_t ld_res
   if (w_post) TRY(check_vec("w_post", w_post, esize(dtype)));
   if (w_pre) TRY(check_vec("w_pre", w_pre, esize(dtype)));
   if (gate) TRY(check_mat("gate", gate, ld_gate == 0 ? d : ld_gate, d, dtype));
-  // the kernels take a pitch for a gate of each token's own: without a gate it is not passed on
-  *a = awq::BlockNormArgs{{y, ld_y}, {residual, ld_residual}, n, (int)d, w_post, w_pre, gate, gate ? ld_gate : 0, res_scale,
-                          eps};
+  // The kernels take a pitch for a gate of each token's own, and zeros times the scale for a y that is not there: neither
+  // is passed on without its matrix.
+  *a = awq::BlockNormArgs{{y, ld_y}, {residual, ld_residual}, n, (int)d, w_post, w_pre, gate, gate ? ld_gate : 0,
+                          y ? res_scale : 1.0f, eps};
   return AWQ_OK;
 }
 

@@ -101,3 +101,11 @@ def test_a_pitch_without_a_gate_is_no_gate_per_token(lib, f):
     assert _launched(lib, lambda: f(lib, gate=None, ld_gate=-5)) and lib.seen_ld_gate() == 0
     assert _launched(lib, lambda: f(lib, gate=FAKE, ld_gate=72)) and lib.seen_ld_gate() == 72
     assert _launched(lib, lambda: f(lib, gate=FAKE)) and lib.seen_ld_gate() == 0
+
+
+@pytest.mark.parametrize("f,parts", [(_norm, dict(res_out=None)), (_norm_backward, dict(d_y=None, d_w_post=None))])
+def test_without_y_there_is_no_residual_scale(lib, f, parts):
+    """r' is the residual then; an infinite scale times the zeros that stand for y would be NaN."""
+    for scale in (0.5, float("inf"), float("nan")):
+        assert _launched(lib, lambda: f(lib, y=None, w_post=None, scale=scale, **parts)) and lib.seen_res_scale() == 1.0
+    assert _launched(lib, lambda: f(lib, scale=0.25)) and lib.seen_res_scale() == 0.25

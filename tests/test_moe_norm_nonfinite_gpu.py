@@ -113,3 +113,16 @@ def test_the_gradient_of_a_block_without_a_norm_does_not_see_its_output(moe, d, 
     for k in ("d_y", "d_residual"):
         within(host(got[k]), want[k], (3 * U * (1 + hs) + hs) * np.abs(want[k]), k)
     within(host(got["d_gate"]), want["d_gate"], 6 * U * 3 * 4, "d_gate")  # three terms of at most a d_res y = 2
+
+
+@pytest.mark.parametrize("scale", [INF, float("nan")])
+@pytest.mark.parametrize("d", [5, 520, 28672])
+def test_without_y_the_residual_scale_is_not_used(moe, d, scale):
+    t, v = _make(d, 3, d, "bf16", y=None, w_post=None, gate=None)
+    ref = moe.awq_block_norm(None, t["residual"], t["w_pre"], eps=EPS)["h"]
+    assert torch.isfinite(ref).all()
+    assert torch.equal(moe.awq_block_norm(None, t["residual"], t["w_pre"], res_scale=scale, eps=EPS)["h"], ref)
+    args = (None, t["residual"], t["d_res"], t["d_h"], t["w_pre"], None, None)
+    ref = moe.awq_block_norm_backward(*args, 1.0, EPS)
+    got = moe.awq_block_norm_backward(*args, scale, EPS)
+    assert all(torch.equal(got[k], ref[k]) for k in ref)
