@@ -32,7 +32,8 @@
  *   - Offsets, positions and orders that a caller changes are checked on the device: an entry outside
  *     its range is skipped or clamped, never followed out of a buffer. Two slots may name the same row where
  *     rows are read (both count); a row that is written holds, element by element, one of the two values.
- *   - Outputs must not overlap inputs unless stated otherwise. Two calls may run at the same time
+ *   - Outputs must not overlap inputs unless stated otherwise; an output that may be an input has its pitch then,
+ *     unless it is one row (AWQ_ERR_ARG). Two calls may run at the same time
  *     unless they share a workspace or an output.
  */
 #ifndef AWQ_MOE_MI355X_H

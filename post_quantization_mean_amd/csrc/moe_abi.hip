@@ -43,6 +43,15 @@ int check_mat(const char* name, const void* p, int64_t ld, int64_t width, int dt
   return AWQ_OK;
 }
 
+// An output that may lie where an input does has to lie there row by row: with another pitch a row's output would cover
+// rows that other blocks still read.
+int check_in_place(const char* name, const void* out, int64_t ld_out, const char* over, const void* in, int64_t ld_in,
+                   int64_t rows) {
+  if (out && out == in && ld_out != ld_in && rows > 1)
+    return fail(AWQ_ERR_ARG, "%s over %s with another pitch (%lld, %lld)", name, over, (ll)ld_out, (ll)ld_in);
+  return AWQ_OK;
+}
+
 int check_vec(const char* name, const void* p, size_t align) {
   if (!p) return fail(AWQ_ERR_NULL, "%s is NULL", name);
   if (!aligned(p, align)) return fail(AWQ_ERR_UNSUPPORTED, "%s is not %zu-byte aligned", name, align);
@@ -187,6 +196,10 @@ int awq_block_norm(const void* y, int64_t ld_y, const void* residual, int64_t ld
   if (res_out) TRY(check_mat("res_out", res_out, ld_res_out, d, dtype));
   if (h) TRY(check_mat("h", h, ld_h, d, dtype));
   if (h && h == res_out) return fail(AWQ_ERR_ARG, "h and res_out are the same buffer");
+  TRY(check_in_place("res_out", res_out, ld_res_out, "y", y, ld_y, n_tokens));
+  TRY(check_in_place("res_out", res_out, ld_res_out, "residual", residual, ld_residual, n_tokens));
+  TRY(check_in_place("h", h, ld_h, "y", y, ld_y, n_tokens));
+  TRY(check_in_place("h", h, ld_h, "residual", residual, ld_residual, n_tokens));
   hipError_t e = awq::launch_block_norm(a, dtype, {res_out, ld_res_out}, {h, ld_h}, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "block_norm launch");
   return ok();
@@ -217,6 +230,8 @@ int awq_block_norm_backward(const void* y, int64_t ld_y, const void* residual, i
   if (d_gate && !gate) return fail(AWQ_ERR_NULL, "d_gate needs gate");
   if (d_y) TRY(check_mat("d_y", d_y, ld_d_y, d, dtype));
   if (d_residual) TRY(check_mat("d_residual", d_residual, ld_d_residual, d, dtype));
+  TRY(check_in_place("d_residual", d_residual, ld_d_residual, "d_res_out", d_res_out, ld_d_res_out, n_tokens));
+  TRY(check_in_place("d_y", d_y, ld_d_y, "d_h", d_h, ld_d_h, n_tokens));
   if (d_w_post) TRY(check_vec("d_w_post", d_w_post, 4));
   if (d_w_pre) TRY(check_vec("d_w_pre", d_w_pre, 4));
   const bool sum_gate = d_gate && ld_gate == 0;
@@ -301,6 +316,7 @@ int awq_moe_combine_backward(const void* d_out, int64_t ld_d_out, const void* ro
   TRY(check_mat("d_out", d_out, ld_d_out, d, dtype));
   TRY(check_mat("rows", rows, ld_rows, d, dtype));
   if (d_rows) TRY(check_mat("d_rows", d_rows, ld_d_rows, d, dtype));
+  TRY(check_in_place("d_rows", d_rows, ld_d_rows, "rows", rows, ld_rows, n_rows));
   if (d_weights) TRY(check_vec("d_weights", d_weights, 4));
   hipError_t e = awq::launch_moe_combine_backward(a, dtype, {d_out, ld_d_out}, {rows, ld_rows}, weights,
                                                   {d_rows, ld_d_rows}, d_weights, (hipStream_t)stream);

@@ -109,3 +109,31 @@ def test_without_y_there_is_no_residual_scale(lib, f, parts):
     for scale in (0.5, float("inf"), float("nan")):
         assert _launched(lib, lambda: f(lib, y=None, w_post=None, scale=scale, **parts)) and lib.seen_res_scale() == 1.0
     assert _launched(lib, lambda: f(lib, scale=0.25)) and lib.seen_res_scale() == 0.25
+
+
+ELSE = FAKE + 0x1000000
+
+
+@pytest.mark.parametrize("f,there", [
+    (_norm, dict(y=ELSE, ld_y=72, res_out=ELSE, ld_ro=64)), (_norm, dict(residual=ELSE, ld_r=72, res_out=ELSE, ld_ro=64)),
+    (_norm, dict(y=ELSE, ld_y=64, h=ELSE, ld_h=72)), (_norm, dict(residual=ELSE, ld_r=64, h=ELSE, ld_h=65)),
+    (_norm_backward, dict(d_res=ELSE, ld_dr=64, d_residual=ELSE, ld_do=80)),
+    (_norm_backward, dict(d_h=ELSE, ld_dh=80, d_y=ELSE, ld_dy=64))])
+def test_in_place_with_another_pitch_is_refused(lib, f, there):
+    """A row's output would lie over rows that other blocks still read. One row has no other, and equal pitches none over it."""
+    apart = dict(y=FAKE, residual=FAKE + 0x10000, res_out=FAKE + 0x20000, h=FAKE + 0x30000) if f is _norm else \
+        dict(d_res=FAKE, d_h=FAKE + 0x10000, d_y=FAKE + 0x20000, d_residual=FAKE + 0x30000)
+    assert _launched(lib, lambda: f(lib, **apart))
+    assert not _launched(lib, lambda: f(lib, **{**apart, **there})) and b"pitch" in lib.awq_last_error()
+    assert _launched(lib, lambda: f(lib, **{**apart, **there}, n=1))
+    same = {k: 72 if k.startswith("ld") else v for k, v in there.items()}
+    assert _launched(lib, lambda: f(lib, **{**apart, **same}))
+
+
+def test_combining_gradients_in_place_with_another_pitch_is_refused(lib):
+    def call(rows, ld_rows, d_rows, ld_d_rows, n_rows=8):
+        return lib.awq_moe_combine_backward(ELSE, 64, rows, ld_rows, BF16, n_rows, 64, FAKE, FAKE, 4, 2, d_rows, ld_d_rows, FAKE,
+                                            None)
+    assert _launched(lib, lambda: call(FAKE, 72, FAKE, 72)) and _launched(lib, lambda: call(FAKE, 72, ELSE, 64))
+    assert not _launched(lib, lambda: call(FAKE, 72, FAKE, 64)) and b"pitch" in lib.awq_last_error()
+    assert _launched(lib, lambda: call(FAKE, 72, FAKE, 64, n_rows=1))
