@@ -167,7 +167,7 @@ typedef enum {
  * dequantized weights of expert e (dequantization and rounding as awq_w4a16_gemm; float32 accumulation;
  * the gated product is formed in float32 and rounded once).
  *   x          [n_rows, ld_x] of x_dtype (AWQ_DTYPE_BF16 or AWQ_DTYPE_F16), 16-byte aligned, ld_x >= d_in
- *              a multiple of 8.
+ *              a multiple of 8 (of a single row any pitch).
  *   codes      uint8 [n_experts, d_out, d_in / 2], 16-byte aligned.
  *   steps_f16  uint16 [n_experts, d_out, d_in / 128], float16 bits.
  *   zeros_u4   uint8 [n_experts, d_out, ceil(d_in / 256)].
@@ -183,7 +183,7 @@ AWQ_API int awq_w4a16_grouped_gemm(const void* x, int64_t ld_x, int x_dtype, con
 /* The gradient of the plain product with respect to its rows (the quantized weights are constants):
  * d_x[i] = d_y[i] W_e, with W_e rounded to dy_dtype as the forward call rounds it to x_dtype.
  *   d_y  [n_rows, ld_d_y] of dy_dtype (AWQ_DTYPE_BF16 or AWQ_DTYPE_F16), 16-byte aligned, ld_d_y >= d_out
- *        a multiple of 8.
+ *        a multiple of 8 (of a single row any pitch).
  *   d_x  [n_rows, ld_d_x] of dx_dtype (AWQ_DTYPE_F32 or dy_dtype), ld_d_x >= d_in.
  * The other arguments as awq_w4a16_grouped_gemm. Any d_out. */
 AWQ_API int awq_w4a16_grouped_gemm_backward(const void* d_y, int64_t ld_d_y, int dy_dtype, const uint8_t* codes,

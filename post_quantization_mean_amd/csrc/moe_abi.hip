@@ -148,8 +148,9 @@ int check_route(int dtype, int64_t n_tokens, int top_k, int64_t d, int64_t n_row
 
 // ---- the experts' products
 
-// `x` is [n_rows, x_width], `y` [n_rows, y_width].
-int check_grouped(const char* x_name, const void* x, int64_t ld_x, int64_t x_width, int x_dtype, const uint8_t* codes,
+// `x` is [n_rows, x_width], `y` [n_rows, y_width]. The pitch of a single row means nothing: *ld_x becomes one that the
+// kernels take.
+int check_grouped(const char* x_name, const void* x, int64_t* ld_x, int64_t x_width, int x_dtype, const uint8_t* codes,
                   const uint16_t* steps, const uint8_t* zeros, const int32_t* offsets, int n_experts, int64_t n_rows,
                   int64_t d_in, int64_t d_out, const char* y_name, void* y, int64_t ld_y, int64_t y_width,
                   int y_dtype) {
@@ -166,14 +167,15 @@ int check_grouped(const char* x_name, const void* x, int64_t ld_x, int64_t x_wid
   TRY(check_vec("steps_f16", steps, 2));
   TRY(check_vec("zeros_u4", zeros, 1));
   TRY(check_vec("offsets", offsets, 4));
-  TRY(check_mat(x_name, x, ld_x, x_width, x_dtype));
+  TRY(check_mat(x_name, x, *ld_x, x_width, x_dtype));
   TRY(check_mat(y_name, y, ld_y, y_width, y_dtype));
-  if (ld_x % 8 || !aligned(x, 16))
+  if (n_rows == 1) *ld_x = (x_width + 7) / 8 * 8;
+  if (*ld_x % 8 || !aligned(x, 16))
     return fail(AWQ_ERR_UNSUPPORTED, "%s must be 16-byte aligned with a pitch of a multiple of 8", x_name);
   // byte offsets inside a tile of 256 rows of x, or of 256 rows of codes, are signed 32-bit
-  if (ld_x > 0x3FFFFF || d_in > 0x3FFF80 || d_out > 0x3FFFFF)
+  if (*ld_x > 0x3FFFFF || d_in > 0x3FFF80 || d_out > 0x3FFFFF)
     return fail(AWQ_ERR_UNSUPPORTED, "%s pitch %lld, d_in %lld or d_out %lld too large for 32-bit tile offsets", x_name,
-                (ll)ld_x, (ll)d_in, (ll)d_out);
+                (ll)*ld_x, (ll)d_in, (ll)d_out);
   if (d_out > 0x7FFFFFFF / (d_in / 2))
     return fail(AWQ_ERR_UNSUPPORTED, "an expert of %lld x %lld weights is too large for 32-bit offsets", (ll)d_out,
                 (ll)d_in);
@@ -331,7 +333,7 @@ int awq_w4a16_grouped_gemm(const void* x, int64_t ld_x, int x_dtype, const uint8
     return fail(AWQ_ERR_ARG, "mode %d is not an awq_grouped_mode", mode);
   const bool gate = mode != AWQ_GROUPED_PLAIN;
   if (gate && d_out % 2) return fail(AWQ_ERR_SHAPE, "d_out %lld of a gate/up pair is odd", (ll)d_out);
-  TRY(check_grouped("x", x, ld_x, d_in, x_dtype, codes, steps_f16, zeros_u4, offsets, n_experts, n_rows, d_in, d_out,
+  TRY(check_grouped("x", x, &ld_x, d_in, x_dtype, codes, steps_f16, zeros_u4, offsets, n_experts, n_rows, d_in, d_out,
                     "y", y, ld_y, gate ? d_out / 2 : d_out, y_dtype));
   const awq::GroupedArgs a{{x, ld_x}, codes, steps_f16, zeros_u4, offsets, n_experts, (int)n_rows, (int)d_in,
                            (int)d_out, mode, {y, ld_y}};
@@ -345,7 +347,7 @@ int awq_w4a16_grouped_gemm_backward(const void* d_y, int64_t ld_d_y, int dy_dtyp
                                     const uint16_t* steps_f16, const uint8_t* zeros_u4, const int32_t* offsets,
                                     int n_experts, int64_t n_rows, int64_t d_in, int64_t d_out, void* d_x,
                                     int64_t ld_d_x, int dx_dtype, void* stream) {
-  TRY(check_grouped("d_y", d_y, ld_d_y, d_out, dy_dtype, codes, steps_f16, zeros_u4, offsets, n_experts, n_rows, d_in,
+  TRY(check_grouped("d_y", d_y, &ld_d_y, d_out, dy_dtype, codes, steps_f16, zeros_u4, offsets, n_experts, n_rows, d_in,
                     d_out, "d_x", d_x, ld_d_x, d_in, dx_dtype));
   const awq::GroupedArgs a{{d_y, ld_d_y}, codes, steps_f16, zeros_u4, offsets, n_experts, (int)n_rows, (int)d_in,
                            (int)d_out, AWQ_GROUPED_PLAIN, {d_x, ld_d_x}};

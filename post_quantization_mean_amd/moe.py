@@ -103,7 +103,7 @@ def _matrix(t, name: str, shape=None, dtype=None, device=None) -> tuple[int, int
     row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its rows")
-    return t.data_ptr(), row if rows > 1 else max(row, cols)
+    return t.data_ptr(), row if rows > 1 else cols  # (the stride of a single row means nothing)
 
 
 def _output(t, name: str, shape, dtype, device):

@@ -137,3 +137,21 @@ def test_combining_gradients_in_place_with_another_pitch_is_refused(lib):
     assert _launched(lib, lambda: call(FAKE, 72, FAKE, 72)) and _launched(lib, lambda: call(FAKE, 72, ELSE, 64))
     assert not _launched(lib, lambda: call(FAKE, 72, FAKE, 64)) and b"pitch" in lib.awq_last_error()
     assert _launched(lib, lambda: call(FAKE, 72, FAKE, 64, n_rows=1))
+
+
+def _grouped(lib, backward, n, ld_x, x=FAKE):
+    """128 inputs and 300 outputs."""
+    mode = () if backward else (0,)
+    f = lib.awq_w4a16_grouped_gemm_backward if backward else lib.awq_w4a16_grouped_gemm
+    return f(x, ld_x, BF16, FAKE, FAKE, FAKE, FAKE, 4, n, 128, 300, *mode, FAKE, 304, F32, None)
+
+
+@pytest.mark.parametrize("backward,width", [(False, 128), (True, 300)])
+def test_the_pitch_of_a_single_row_means_nothing(lib, backward, width):
+    for ld in (width, width + 3, width + 4, 1 << 23):
+        assert _launched(lib, lambda: _grouped(lib, backward, 1, ld)), ld
+        assert lib.seen_ld_x() == (width + 7) // 8 * 8  # rows past the last one lie past the row's end for the kernels
+        assert _launched(lib, lambda: _grouped(lib, backward, 2, ld)) == (ld % 8 == 0 and ld < 1 << 22)
+    assert not _launched(lib, lambda: _grouped(lib, backward, 1, width - 1))
+    assert not _launched(lib, lambda: _grouped(lib, backward, 1, width, FAKE + 8))
+    assert _launched(lib, lambda: _grouped(lib, backward, 2, 304)) and lib.seen_ld_x() == 304
