@@ -416,7 +416,8 @@ def awq_w4a16_grouped_gemm_backward(d_y: torch.Tensor, codes: torch.Tensor, step
                                     zeros_u4: torch.Tensor, offsets: torch.Tensor, out_dtype=None, dx=None,
                                     stream=None) -> torch.Tensor:
     """d_x [n_rows, d_in]: row i of d_y ([n_rows, d_out]) times its expert's dequantized weights, not
-    transposed: the gradient of the plain product with respect to x."""
+    transposed: the gradient of the plain product with respect to x. The kernels take rows that start at 16-byte
+    boundaries: a d_y whose rows do not (a contiguous one where d_out is no multiple of 8) is copied to ones that do."""
     if stream is not None:
         return _on_stream(stream, awq_w4a16_grouped_gemm_backward, d_y, codes, steps_f16, zeros_u4, offsets, out_dtype,
                           dx)
@@ -424,6 +425,11 @@ def awq_w4a16_grouped_gemm_backward(d_y: torch.Tensor, codes: torch.Tensor, step
     ptrs, e, d_in, d_out = _export_args(d_y, codes, steps_f16, zeros_u4, offsets)
     pd, ldd = _matrix(d_y, "d_y", (d_y.shape[0], d_out) if d_y.dim() == 2 else None)
     n = d_y.shape[0]
+    if pd % 16 or (ldd % 8 and n > 1):
+        ldd = (d_out + 7) // 8 * 8
+        rows = torch.empty(n, ldd, dtype=d_y.dtype, device=d_y.device)
+        rows[:, :d_out].copy_(d_y)
+        pd = rows.data_ptr()
     dx, px, ldx, xd = _grouped_output(d_y, dx, "dx", (n, d_in), out_dtype)
     _call(lib.awq_w4a16_grouped_gemm_backward, d_y.device, pd, ldd, _DTYPES[d_y.dtype], *ptrs, e, n, d_in, d_out,
           px, ldx, xd)
