@@ -231,6 +231,8 @@ def _workspace(nbytes: int, device, workspace):
     _dev(workspace, "workspace")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the other operands on {device}")
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, {nbytes} needed")
     return workspace
