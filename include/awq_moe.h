@@ -138,7 +138,7 @@ AWQ_API int awq_moe_gather_backward(const void* d_rows, int64_t ld_d_rows, int d
                                     void* stream);
 
 /* out[t] = sum over the kept slots of token t, in order, of weights[t, j] * rows[position[t, j]] (zeros
- * for a token without any; the weights of dropped slots are not read).
+ * for a token without any; the weights of dropped slots may hold anything and are not used).
  *   weights  float32 [n_tokens, top_k]. */
 AWQ_API int awq_moe_combine(const void* rows, int64_t ld_rows, int dtype, int64_t n_rows, int64_t d,
                             const int32_t* position, const float* weights, int64_t n_tokens, int top_k, void* out,
@@ -147,7 +147,8 @@ AWQ_API int awq_moe_combine(const void* rows, int64_t ld_rows, int dtype, int64_
 /* The gradients of awq_moe_combine:
  *   d_rows[position[t, j]] = weights[t, j] * d_out[t]            (other rows are left as they were)
  *   d_weights[t, j]        = sum over d of d_out[t] * rows[position[t, j]]    (0 for a dropped slot)
- *   d_rows     [n_rows, ld_d_rows] of dtype, or NULL.  May be rows.
+ *   d_rows     [n_rows, ld_d_rows] of dtype, or NULL. May be rows, unless two slots name the same row (the
+ *              second's d_weights would see the first's gradient).
  *   d_weights  float32 [n_tokens, top_k], or NULL. */
 AWQ_API int awq_moe_combine_backward(const void* d_out, int64_t ld_d_out, const void* rows, int64_t ld_rows, int dtype,
                                      int64_t n_rows, int64_t d, const int32_t* position, const float* weights,

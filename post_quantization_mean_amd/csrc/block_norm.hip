@@ -7,8 +7,9 @@
 // stride: the [d] weights stay in its registers, and the next row is loaded while the current one is
 // summed, so that loads stay in flight across the sums' barriers. The gradients of the [d] weights gather in
 // registers over the block's rows, then over blocks in a second kernel, in a fixed order: no atomics.
-// Measured: forward 8192 x 8192 bf16 103 us (5.2 TB/s), 8192 x 4096 47 (5.7); gradients 8192 x 4096 bf16 98 (4.1: two
-// blocks of 512 threads fill the registers of a compute unit), float32 157 (5.1).
+// Measured: forward 8192 x 8192 bf16 101 us (5.3 TB/s), 8192 x 4096 47 (5.7); gradients 8192 x 4096 bf16 97 (4.1: two
+// blocks of 256 threads fill the registers of a compute unit), float32 155 (5.2). At 8192 x 4100 a row's last chunk needs a
+// fifth wave and a compute unit holds one block: 143.
 #include <type_traits>
 
 #include "awq_moe.h"
@@ -68,8 +69,9 @@ struct Places {
 };
 
 // KEEP: the weights stay in registers and the next row is loaded ahead; otherwise (wide rows) neither, which
-// the registers would not hold: weights and gate are loaded a chunk at a time. 1170 x 28672 bf16 57 us (4.7 TB/s; whole
-// rows of weights spilled, 92), 2048 x 16384 float32 104 (5.2; 125), 1170 x 28672 float32, which still spills, 245 (2.2).
+// the registers would not hold: weights and gate are loaded a chunk at a time. 1170 x 28672 bf16 57 - 60 us (4.5 - 4.7 TB/s;
+// whole rows of weights spilled, 92), 2048 x 16384 float32 104 - 113 (4.8 - 5.2; 125), 1170 x 28672 float32, which still
+// spills, 234 - 238 (2.3).
 template <typename T, int ITEMS, int TMAX, bool KEEP>
 __global__ __launch_bounds__(TMAX) void block_norm_kernel(BlockNormArgs a, Mat res_out, Mat h) {
   constexpr int V = kVec<T>;
@@ -316,7 +318,6 @@ __global__ __launch_bounds__(512) void block_norm_backward_kernel(BlockNormArgs 
       if (g.d_residual.p) store_own((T*)g.d_residual.p + row * g.d_residual.ld, at.p[i], D);
       if (TOKEN && g.d_gate.p) store_own((T*)g.d_gate.p + row * g.d_gate.ld, at.p[i], dg);
     }
-    // the next row's loads: only y of this row is still needed
     if (g.d_y.p) {
       float m1 = 0.f;
       if (a.w_post) {
@@ -357,8 +358,8 @@ __global__ __launch_bounds__(512) void block_norm_backward_kernel(BlockNormArgs 
 // Rows too wide for the registers of a block, or narrower than a chunk, take two kernels: the first finds each
 // row's norms and means (reading the row again in every pass, from the caches), with which the second is
 // element-wise: its blocks walk down strips of columns, write the rows' gradients and keep the sums over tokens
-// in registers. 14 passes instead of 6, of which the caches serve some: 1170 x 28672 bf16 189 us, 3048 x 11008 177,
-// 1170 x 28672 float32 340 (with loads behind branches 458, 419, 391).
+// in registers. 14 passes instead of 6, of which the caches serve some: 1170 x 28672 bf16 183 - 193 us, 3048 x 11008 181,
+// 1170 x 28672 float32 340 - 348 (with loads behind branches 458, 419, 391).
 struct RowStats {
   float rs1, rs2, m2, m1;  // m1: mean(t u1) rs1, times y in d_y
 };
@@ -375,7 +376,7 @@ struct WideChunk {
   __device__ __forceinline__ WideChunk(int first, int width) : at(first, width), c(first), d(width) {}
   __device__ __forceinline__ bool owns(int k) const { return SMALL ? c + k < d : k >= at.skip; }
   __device__ __forceinline__ int column(int k) const { return SMALL ? c + k : at.at + k; }
-  // `none` also for elements of the chunk before
+  // `none` where the input is not given (elements of the chunk before hold the neighbour's values: owns())
   __device__ __forceinline__ void get(const void* p, const void* instead, int64_t offset, float none,
                                       float (&v)[V]) const {
     const T* row = p ? (const T*)p + offset : (const T*)instead;

@@ -90,9 +90,10 @@ __device__ __forceinline__ float gated(float g, float u, int mode) {
 // brings a row's eight steps. With the rows in LDS the codes are the only loads that a wave waits for (the counter
 // of outstanding loads completes in issue order, so a load of activations behind codes would wait for these too),
 // and no load sits behind a branch, where the compiler would wait for it at once. The KS waves' partial products
-// are added at the end, in wave order. Bound by the dequantization's VALU work (22 instructions for 8 weights): one
-// token's gate and up products of 2 of 8 experts of 4096 x 22016 take 25 us (3.7 TB/s; one wave over the whole
-// contraction 37), 48 tokens' of 4 of 32 experts of 2048 x 2048 20.
+// are added at the end, in wave order. Bound by the latency of its loads and the ramp of a short kernel: one token's gate
+// and up products of 2 of 8 experts of 4096 x 22016 take 25 us (3.7 TB/s; one wave over the whole contraction 37) with the
+// VALU 45 % busy, the matrix units 7 % and 1.01 times the bytes fetched past L2; 48 tokens' of 4 of 32 experts of
+// 2048 x 2048 take 20 - 21 with 37 %, 6 % and 1.1 times.
 constexpr int kRing = 2;
 constexpr int kChunkGroups = 8;
 constexpr int kStreamWaves = 4;
@@ -300,9 +301,12 @@ __global__ __launch_bounds__(64 * kStreamWaves, 5) void grouped_stream_kernel(Gr
 // 16 MT rows of one expert against its weights: each wave streams the codes of 32 output rows (GATED: 16 and 16)
 // through registers as above, each dequantized fragment multiplying MT row tiles. The rows come through LDS a group
 // (128 inputs) at a time, by DMA two groups ahead into a ring of four stages. Loads complete in issue order, and a
-// group's codes are sent for right behind its rows: with the codes in hand, so is the wave's share of the rows. Few rows
-// are bound by the dequantization, 64 by the matrix instructions and LDS reads beside it: 8 experts of 4096 x 22016
-// with 32 rows each take 131 us (2.8 TB/s of weights, 350 TFLOP/s), with 128 rows 324 (570 TFLOP/s).
+// group's codes are sent for right behind its rows: with the codes in hand, so is the wave's share of the rows. With many
+// waves, bound by the memory and the dequantization in turn, then by the matrix instructions and LDS reads beside it: 8
+// experts of 4096 x 22016 with 4 rows each take 97 us (4.6 TB/s fetched; VALU 62 % busy), with 32 rows 125 - 131 (3.0 TB/s of
+// weights, 370 TFLOP/s; VALU 49 %, matrix units 30 %), with 128 rows 280 - 324. With few, by latency: a group waits for loads
+// that were sent for two groups before, 0.8 us a group whatever the rows and columns are: one expert of 11008 x 4096 with 10
+// rows takes 70 us (VALU 4 %), of 4096 x 512 with 100 rows 28.
 template <int KIND, typename OutT, bool GATED, int W, int MT>
 __global__ __launch_bounds__(64 * W) void grouped_mid_kernel(GroupedArgs a) {
   constexpr int C = kChunkGroups, kStages = 4, kStageBytes = 16 * MT * 256;
@@ -408,8 +412,9 @@ __device__ __forceinline__ float row_bcast(float v) {
 // that its eight column tiles j (column 8 n + j in column place n) each find their eight consecutive k in the lane's
 // own registers: the transposition costs no exchange. Lane n also brings the step and zero point of row o + 8 kq + n mod 8,
 // which the lanes of its group take from it. Everything for the next block is loaded before this one is multiplied.
-// Bound by the dequantization and the matrix instructions in turn: 8 experts of 22016 x 4096 with 32 rows each take
-// 174 us (2.1 TB/s of weights, 265 TFLOP/s).
+// Bound by what comes in past the L2s: 8 experts of 22016 x 4096 with 4 or 32 rows each take 167 - 174 us and fetch 2.3 - 2.5
+// times the weights' bytes (870 - 960 MB, 5.1 - 5.7 TB/s), since a block reads 64 of the 128 bytes of a line of codes and 2 of
+// one of steps, and the blocks that read the rest lie on other XCDs. The VALU is 37 - 43 % busy, the matrix units 5 - 22 %.
 constexpr int kBackwardWaves = 8;
 
 template <int KIND, typename OutT, int MT>

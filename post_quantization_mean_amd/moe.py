@@ -4,8 +4,9 @@ As in `binding`, every function has the name of the C entry point it calls and o
 outputs are allocated unless given. Work goes to torch's current stream of the tensors' device. With `stream`
 (a stream of that device) a call does what it does inside `torch.cuda.stream(stream)`: outputs and workspaces
 are allocated there too, and what is passed has to be ready on that stream and to outlive its work; an output that
-is used on another stream has to wait for it. The *_backward functions are the gradients; the quantized weights
-and the input multipliers are constants.
+is used on another stream has to wait for it. No call records a graph for autograd: outputs do not require a
+gradient even where inputs do, and the *_backward functions are the gradients, for a program that calls them itself;
+the quantized weights and the input multipliers are constants.
 """
 from __future__ import annotations
 
@@ -335,7 +336,8 @@ def awq_moe_combine(rows: torch.Tensor, position: torch.Tensor, weights: torch.T
 def awq_moe_combine_backward(d_out: torch.Tensor, rows: torch.Tensor, position: torch.Tensor, weights: torch.Tensor,
                              out=None, stream=None) -> dict:
     """{"d_rows": weights[t, j] * d_out[t] at position[t, j], "d_weights": <d_out[t], rows[position[t, j]]>}.
-    `out` may hold either; rows of d_rows that no slot names are left as they were."""
+    `out` may hold either (d_rows also rows itself, where no two slots name the same row); rows of d_rows that no slot
+    names are left as they were."""
     if stream is not None:
         return _on_stream(stream, awq_moe_combine_backward, d_out, rows, position, weights, out)
     lib = _load()
