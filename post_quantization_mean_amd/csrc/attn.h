@@ -1,0 +1,84 @@
+// Internal declarations of attention over the 4-bit cache (rope.hip, kv4_cache.hip, kv4_attention.hip), shared with its
+// host-side C ABI (attn_abi.hip). Not part of the public interface (include/awq_attn.h is).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace awq {
+
+// A [tokens, heads, channels] argument: pitches in elements.
+struct Heads {
+  void* p;
+  int64_t ld, ld_head;
+};
+struct CHeads {
+  const void* p;
+  int64_t ld, ld_head;
+};
+
+struct RopeArgs {
+  CHeads x;
+  Heads out;
+  int64_t n_tokens;
+  int n_heads, head_dim, rot_dim;
+  const void* positions;
+  int64_t ld_positions;
+  bool pos64;
+  int n_axes;
+  const float* inv_freq;
+  const int32_t* axis;
+  float cos_scale, sin_scale;  // sin_scale = -cos_scale: the gradient
+  bool in_place;
+};
+hipError_t launch_rope(const RopeArgs& a, int dtype, bool pairs, hipStream_t stream);
+
+// The cache: pitches from page to page in bytes of codes and in words of params (one word: step, offset).
+struct Kv4Cache {
+  uint8_t* codes;
+  uint32_t* params;
+  int64_t page_codes, page_params;
+  int64_t n_pages;
+  int page_log2, n_kv, head_dim, n_groups;
+};
+
+struct Kv4MoveArgs {
+  Kv4Cache c;
+  const void* slots;
+  bool slots64;
+  int64_t n_tokens;
+};
+hipError_t launch_kv4_write(const Kv4MoveArgs& a, int dtype, CHeads k, CHeads v, hipStream_t stream);
+hipError_t launch_kv4_read(const Kv4MoveArgs& a, int dtype, Heads k, Heads v, hipStream_t stream);
+
+struct AttnArgs {
+  Kv4Cache c;
+  CHeads q;
+  Heads out;
+  bool out_f32;
+  float* lse;
+  const int32_t *table, *kv_len, *q_offsets;
+  int64_t ld_table;
+  int table_width, n_seqs, n_heads;
+  int64_t n_tokens;
+  int group;     // query heads of a key head
+  int each;      // new tokens of each sequence where q_offsets is NULL
+  float scale;   // times log2(e)
+  int causal;
+  int window;    // 0: none
+  int max_kv;
+  // how the work is split (plan_attention)
+  int tile_rows;   // (token, head) rows of a key head that a block takes
+  int n_tiles;     // tiles of rows over all sequences, at most
+  int chunk;       // cached tokens of a block, at least (a multiple of 32)
+  int n_chunks;    // blocks along a sequence
+  float* part_o;   // [n_chunks][n_tokens * n_heads][head_dim], with n_chunks > 1
+  float* part_ml;  // [n_chunks][n_tokens * n_heads][2]
+};
+
+// Fills the split from the sizes; returns the workspace's floats (part_o, then part_ml).
+size_t plan_attention(AttnArgs* a, bool ragged);
+hipError_t launch_kv4_attention(const AttnArgs& a, bool bf16, hipStream_t stream);
+
+}  // namespace awq
