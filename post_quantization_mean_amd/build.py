@@ -21,7 +21,8 @@ ARCH = "gfx950"
 
 SOURCES = ["act_stats.hip", "scales.hip", "quant.hip", "err_gemm.hip", "export.hip", "variants.hip", "w4a16.hip", "block_gemm.hip", "gram.hip", "abi.hip",
            "block_norm.hip", "moe_route.hip", "w4a16_grouped.hip", "moe_abi.hip",
-           "rope.hip", "kv4_cache.hip", "kv4_attention.hip", "attn_abi.hip"]
+           "rope.hip", "kv4_cache.hip", "kv4_attention.hip", "kv4_prompt.hip",
+           "attn_abi.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

@@ -1,4 +1,4 @@
-// Internal declarations of attention over the 4-bit cache (rope.hip, kv4_cache.hip, kv4_attention.hip), shared with its
+// Internal declarations of attention over the 4-bit cache (rope.hip, kv4_cache.hip, kv4_attention.hip, kv4_prompt.hip), shared with its
 // host-side C ABI (attn_abi.hip). Not part of the public interface (include/awq_attn.h is).
 #pragma once
 
@@ -79,6 +79,9 @@ struct AttnArgs {
 
 // Fills the split from the sizes; returns the workspace's floats (part_o, then part_ml).
 size_t plan_attention(AttnArgs* a, bool ragged);
+// tile_rows of the kernel for prompts
+constexpr int prompt_rows(int head_dim) { return head_dim <= 128 ? 256 : 128; }
+hipError_t launch_kv4_prompt(const AttnArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_kv4_attention(const AttnArgs& a, bool bf16, hipStream_t stream);
 
 }  // namespace awq

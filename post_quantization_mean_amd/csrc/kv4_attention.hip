@@ -110,16 +110,9 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const RowTile& t
         nan = fmaf(x[s][k], 0.f, nan);
       }
     }
-    // bfloat16 reaches past float16: each row is brought to a largest magnitude in [1, 2) by a power of two, which the
-    // scale of its scores takes back. What then lies below float16's normal numbers is 2^-14 of the row's largest.
-    float up = 1.f, down = 1.f;
-    if constexpr (BF16) {
-      const int e = (int)(__float_as_uint(max_over_rows(top)) >> 23) - 127;
-      const int f = min(max(e, -126), 126);
-      up = __uint_as_float((uint32_t)(127 - f) << 23);
-      down = __uint_as_float((uint32_t)(127 + f) << 23);
-    }
-    scale[n] = a.scale * down + sum_over_rows(nan);  // NaN for a row with a NaN or an infinity
+    float up, down;
+    query_range<BF16>(max_over_rows(top), a.scale, up, down);
+    scale[n] = fmaxf(fabsf(a.scale) * down, 0x1p-126f) + sum_over_rows(nan);  // NaN for a row with a NaN or an infinity
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s) {
       constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
@@ -241,7 +234,7 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[4 * h + j] = s[n][h][j] * scale[n];
+        for (int j = 0; j < 4; ++j) x[4 * h + j] = s[n][h][j];
       if (!whole) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -253,7 +246,7 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmaxf(most, x[j]);
-      most = max_over_rows(most);
+      most = max_over_rows(most) * scale[n];
       // The numerators are powers from a reference that is set 2^7 below the largest score and moves only when they would
       // pass 2^15: float16 holds them, down to 2^-31 of the largest.
       if (__any(most > top[n] + 15.f)) {
@@ -267,7 +260,8 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         // rounded towards zero, and summed as rounded: the weights add up to one, and the rounding's bias cancels
-        const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(x[j] - top[n]), __builtin_amdgcn_exp2f(x[j + 1] - top[n]));
+        const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(fmaf(x[j], scale[n], -top[n])),
+                                                    __builtin_amdgcn_exp2f(fmaf(x[j + 1], scale[n], -top[n])));
         const h2 pair = __builtin_bit_cast(h2, two);
         sum[n] = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum[n], false);
         p[n][j] = pair.x;
@@ -376,12 +370,8 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
         }
         const int64_t to = (t.token0 + token) * a.out.ld + (int64_t)of * a.out.ld_head + c;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float z = y[k] * inv;
-          if (a.out_f32) ((float*)a.out.p)[to + k] = z;
-          else if (BF16) ((Bf16*)a.out.p)[to + k] = from_f32<Bf16>(z);
-          else ((F16*)a.out.p)[to + k] = from_f32<F16>(z);
-        }
+        for (int k = 0; k < 4; ++k) y[k] *= inv;
+        store4<BF16>(a, to, y);
       }
     }
   }
@@ -455,17 +445,23 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   if (a.c.head_dim <= 64) launch_rows<64, BF16>(a, stream);
   else if (a.c.head_dim <= 128) launch_rows<128, BF16>(a, stream);
   else launch_rows<256, BF16>(a, stream);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.n_chunks == 1) return e;
+  return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
   join_kernel<BF16><<<dim3((unsigned)a.n_tiles, (unsigned)a.c.n_kv, (unsigned)a.tile_rows), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Rows of a sequence and key head up to which a block of the kernel above takes 32 of them; past that the kernel for prompts.
+constexpr int kFewRows = 64;
+
 size_t plan_attention(AttnArgs* a, bool ragged) {
   const int64_t rows_each = (a->n_tokens + a->n_seqs - 1) / a->n_seqs * a->group;
-  a->tile_rows = rows_each <= 16 ? 16 : 32;
+  a->tile_rows = rows_each <= 16 ? 16 : rows_each <= kFewRows ? 32 : prompt_rows(a->c.head_dim);
   if (ragged) a->n_tiles = (int)(a->n_tokens * a->group / a->tile_rows + a->n_seqs);
   else a->n_tiles = (int)(a->n_seqs * ((rows_each + a->tile_rows - 1) / a->tile_rows));
   int64_t span = a->max_kv;
@@ -482,7 +478,9 @@ size_t plan_attention(AttnArgs* a, bool ragged) {
 }
 
 hipError_t launch_kv4_attention(const AttnArgs& a, bool bf16, hipStream_t stream) {
-  return bf16 ? launch<true>(a, stream) : launch<false>(a, stream);
+  hipError_t e = a.tile_rows > 32 ? launch_kv4_prompt(a, bf16, stream) : bf16 ? launch<true>(a, stream) : launch<false>(a, stream);
+  if (e != hipSuccess || a.n_chunks == 1) return e;
+  return bf16 ? launch_join<true>(a, stream) : launch_join<false>(a, stream);
 }
 
 }  // namespace awq

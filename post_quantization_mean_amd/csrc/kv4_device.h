@@ -109,6 +109,34 @@ __device__ __forceinline__ h8 token_codes(uint32_t w, h2 step, h2 offset) {
   return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
+// bfloat16 queries reach past float16: each row is brought to a largest magnitude in [1, 2) by a power of two (`up`), which the
+// scale of its scores takes back (`down`). What then lies below float16's normal numbers is below 2^-14 of the row's
+// largest. Negative scales are moved into the queries, so that the largest product is the largest score.
+template <bool BF16>
+__device__ __forceinline__ void query_range(float largest, float scale, float& up, float& down) {
+  up = down = 1.f;
+  if constexpr (BF16) {
+    const int e = min(max((int)(__float_as_uint(largest) >> 23) - 127, -126), 126);
+    up = __uint_as_float((uint32_t)(127 - e) << 23);
+    down = __uint_as_float((uint32_t)(127 + e) << 23);
+  }
+  if (scale < 0.f) up = -up;
+}
+
+// Four consecutive channels of the output, element `to` on.
+template <bool BF16>
+__device__ __forceinline__ void store4(const AttnArgs& a, int64_t to, const float (&y)[4]) {
+  if (a.out_f32) {
+    struct __attribute__((packed, aligned(4))) Four { float v[4]; };
+    *reinterpret_cast<Four*>((float*)a.out.p + to) = Four{{y[0], y[1], y[2], y[3]}};
+  } else {
+    struct __attribute__((packed, aligned(2))) Four { uint16_t v[4]; } u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u.v[k] = BF16 ? from_f32<Bf16>(y[k]).v : from_f32<F16>(y[k]).v;
+    *reinterpret_cast<Four*>((uint16_t*)a.out.p + to) = u;
+  }
+}
+
 // max or sum over the four rows of 16 lanes, in every lane
 __device__ __forceinline__ float max_over_rows(float v) {
   const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
