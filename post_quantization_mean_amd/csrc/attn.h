@@ -52,6 +52,22 @@ struct Kv4MoveArgs {
 hipError_t launch_kv4_write(const Kv4MoveArgs& a, int dtype, CHeads k, CHeads v, hipStream_t stream);
 hipError_t launch_kv4_read(const Kv4MoveArgs& a, int dtype, Heads k, Heads v, hipStream_t stream);
 
+// Division of 0 <= n < 2^31 by a number known on the host: one multiplication (the quotient of n and the divisor is that of
+// n * (2^32 + mul) and 2^(32 + shift)).
+struct Divisor {
+  uint32_t mul, shift;
+  Divisor(uint32_t d = 1) {
+    shift = 0;
+    while (((uint64_t)1 << shift) < d) ++shift;
+    mul = (uint32_t)((((((uint64_t)1 << shift) - d) << 32) / d) + 1);
+  }
+#ifdef __HIPCC__
+  __device__ __forceinline__ int of(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+#endif
+};
+
+constexpr int kUnit = 128;  // cached tokens that the split counts in
+
 struct AttnArgs {
   Kv4Cache c;
   CHeads q;
@@ -69,16 +85,19 @@ struct AttnArgs {
   int window;    // 0: none
   int max_kv;
   // how the work is split (plan_attention)
-  int tile_rows;   // (token, head) rows of a key head that a block takes
+  int tile_rows;   // (token, head) rows of a key head that a block takes: a power of two
+  int tile_log2;
   int n_tiles;     // tiles of rows over all sequences, at most
-  int chunk;       // cached tokens of a block, at least (a multiple of 32)
-  int n_chunks;    // blocks along a sequence
-  float* part_o;   // [n_chunks][n_tokens * n_heads][head_dim], with n_chunks > 1
-  float* part_ml;  // [n_chunks][n_tokens * n_heads][2]
+  int n_blocks;    // 0: a block for each tile and key head; else blocks that share the cached tokens evenly (kv4_device.h)
+  Divisor by_group, by_tiles, by_kv;  // by group, by the tiles of each sequence (where q_offsets is NULL), by n_kv
+  int* prefix;     // with n_blocks: [n_tiles + 1] (the workspace's start)
+  float* part_o;   // [2 n_blocks][tile_rows][head_dim]
+  float* part_ml;  // [2 n_blocks][tile_rows][2]
 };
 
-// Fills the split from the sizes; returns the workspace's floats (part_o, then part_ml).
+// Fills the split from the sizes; returns the workspace's bytes.
 size_t plan_attention(AttnArgs* a, bool ragged);
+void place_workspace(AttnArgs* a, void* workspace);
 // tile_rows of the kernel for prompts
 constexpr int prompt_rows(int head_dim) { return head_dim <= 128 ? 256 : 128; }
 hipError_t launch_kv4_prompt(const AttnArgs& a, bool bf16, hipStream_t stream);

@@ -172,7 +172,7 @@ int check_attention_sizes(int64_t n_tokens, int64_t n_seqs, bool ragged, int64_t
 }
 
 awq::AttnArgs attention_plan(int64_t n_tokens, int64_t n_seqs, bool ragged, int64_t n_heads, int64_t n_kv, int64_t head_dim,
-                             int causal, int64_t window, int64_t max_kv, size_t* floats) {
+                             int causal, int64_t window, int64_t max_kv, size_t* bytes) {
   awq::AttnArgs a = {};
   a.c.n_kv = (int)n_kv;
   a.c.head_dim = (int)head_dim;
@@ -184,7 +184,7 @@ awq::AttnArgs attention_plan(int64_t n_tokens, int64_t n_seqs, bool ragged, int6
   a.causal = causal;
   a.window = (int)(window < kMostKv ? window : kMostKv);
   a.max_kv = (int)(max_kv < 1 ? 1 : max_kv < kMostKv ? max_kv : kMostKv);
-  *floats = awq::plan_attention(&a, ragged);
+  *bytes = round_up(awq::plan_attention(&a, ragged), 256);
   return a;
 }
 
@@ -253,9 +253,9 @@ size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int r
     ok();  // a query leaves no error behind
     return 0;
   }
-  size_t floats;
-  attention_plan(n_tokens, n_seqs, ragged != 0, n_heads, n_kv, head_dim, causal, window, max_kv, &floats);
-  return round_up(floats * sizeof(float), 256);
+  size_t bytes;
+  attention_plan(n_tokens, n_seqs, ragged != 0, n_heads, n_kv, head_dim, causal, window, max_kv, &bytes);
+  return bytes;
 }
 
 int awq_kv4_attention(const void* q, int64_t ld_q, int64_t ld_q_head, int q_dtype, int64_t n_tokens, int64_t n_heads,
@@ -285,16 +285,16 @@ int awq_kv4_attention(const void* q, int64_t ld_q, int64_t ld_q_head, int q_dtyp
   if (out == q && out_dtype != q_dtype) return fail(AWQ_ERR_ARG, "out over q of another type");
   TRY(check_in_place("out", out, ld_out, ld_out_head, "q", q, ld_q, ld_q_head, n_tokens, n_heads));
   if (lse) TRY(check_vec("lse", lse, 4));
-  size_t floats;
+  size_t need;
   awq::AttnArgs a = attention_plan(n_tokens, n_seqs, q_offsets != nullptr, n_heads, n_kv, head_dim, causal, window,
-                                   max_kv ? max_kv : table_width * page_size, &floats);
-  const size_t need = round_up(floats * sizeof(float), 256);
+                                   max_kv ? max_kv : table_width * page_size, &need);
+  // units of the split are counted in 32 bits; tables that could hold more are not split
+  if ((int64_t)a.n_tiles * n_kv * (table_width * page_size / awq::kUnit + 1) > 0x7FFFFFFF) a.n_blocks = 0, need = 0;
   if (need) {
     if (!workspace || workspace_bytes < need)
       return fail(AWQ_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
     if (!aligned(workspace, 256)) return fail(AWQ_ERR_UNSUPPORTED, "the workspace is not 256-byte aligned");
-    a.part_o = (float*)workspace;
-    a.part_ml = a.part_o + (size_t)a.n_chunks * (size_t)n_tokens * (size_t)n_heads * (size_t)head_dim;
+    awq::place_workspace(&a, workspace);
   }
   a.c = c;
   a.q = {q, ld_q, ld_q_head};

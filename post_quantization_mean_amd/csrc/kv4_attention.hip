@@ -12,6 +12,7 @@
 //                 two tokens' bytes beside each other are pairs of the contraction, channel by channel.
 // So no operand crosses a lane, and nothing goes through LDS until the waves join. Codes become float16 numbers offset +
 // code * step with one rounding (2^-11 of the number at most); 1.7 vector operations a code.
+
 #include <type_traits>
 
 #include "kv4_device.h"
@@ -38,17 +39,17 @@ struct Loader {
   const uint32_t* params;
   int64_t page_codes, page_params, v_codes, v_params;  // from keys to values
   const int32_t* table;
-  int page_log2, page_mask, row_bytes, lane_pages;
+  int page_log2, page_mask, row_bytes, lane_pages, lane;
   uint32_t n_pages;
   int k_at[(HD + 127) / 128], v_at, k_group, v_group;  // this lane's bytes of a row, its groups' params (in words)
 
   // The pages of the wave's next 64 tiles of 16 tokens: lane i has tile i's (-1 past the end).
   __device__ __forceinline__ void pages(int t0, int stride, int end) {
-    const int lane = threadIdx.x & 63, t = t0 + (lane >> 1) * stride + (lane & 1) * 16;
+    const int t = t0 + (lane >> 1) * stride + (lane & 1) * 16;
     lane_pages = t < end ? table[t >> page_log2] : -1;
   }
   __device__ __forceinline__ void load(Stage<HD>& s, int i, int t0) const {
-    const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const int g = lane >> 4, m = lane & 15;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int id = __builtin_amdgcn_readlane(lane_pages, 2 * i + h);
@@ -86,28 +87,40 @@ struct Loader {
   }
 };
 
-// A lane's part of the queries' operand: rows m of NR tiles, channels g * HD/4 .. in the order of token_codes.
-template <int HD, int NR, bool BF16>
-__device__ __forceinline__ void load_queries(const AttnArgs& a, const RowTile& t, int head, h8 (&q)[NR][HD / 32], float (&scale)[NR]) {
-  using T = typename std::conditional<BF16, Bf16, F16>::type;
-  const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+// A lane's part of the queries: rows m of NR tiles, channels g * HD/4 .. . Zeros past the last row and channel.
+template <int HD, int NR, typename T>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const RowTile& t, int head, int lane, uint4 (&raw)[NR][HD / 32]) {
+  const int g = lane >> 4, m = lane & 15;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    const int r = t.row0 + 16 * n + m;
-    const bool there = r < t.rows;
-    const int token = r / a.group, of = r - token * a.group;
-    const T* row = (const T*)a.q.p + (t.token0 + token) * a.q.ld + (int64_t)(head * a.group + of) * a.q.ld_head;
-    float x[HD / 32][8], top = 0.f, nan = 0.f;
+    const int r = min(t.row0 + 16 * n + m, t.rows - 1);
+    const int token = a.by_group.of(r), of = r - token * a.group;
+    const T* row = (const T*)a.q.p + (int64_t)(t.token0 + token) * a.q.ld + (int64_t)(head * a.group + of) * a.q.ld_head;
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s) {
       const int c = g * (HD / 4) + s * 8;
+      raw[n][s] = __builtin_bit_cast(uint4, *reinterpret_cast<const Chunk<T>*>(row + (c < a.c.head_dim ? c : 0)));
+    }
+  }
+}
+
+// Their operand, in the order of token_codes, and what their scores are multiplied by (times log2(e)).
+template <int HD, int NR, bool BF16, typename T>
+__device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile& t, int lane, uint4 (&raw)[NR][HD / 32],
+                                                h8 (&q)[NR][HD / 32], float (&scale)[NR]) {
+  const int g = lane >> 4, m = lane & 15;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[s][k] = 0.f;
-      if (there && c < a.c.head_dim) load_chunk(row, c, a.c.head_dim, x[s]);
+  for (int n = 0; n < NR; ++n) {
+    const bool there = t.row0 + 16 * n + m < t.rows;
+    float top = 0.f, nan = 0.f;
+#pragma unroll
+    for (int s = 0; s < HD / 32; ++s) {
+      if (!there || g * (HD / 4) + s * 8 >= a.c.head_dim) raw[n][s] = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        top = fmaxf(top, fabsf(x[s][k]));
-        nan = fmaf(x[s][k], 0.f, nan);
+        const float x = raw_f32<T>(raw[n][s], k);
+        top = fmaxf(top, fabsf(x));
+        nan = fmaf(x, 0.f, nan);
       }
     }
     float up, down;
@@ -117,30 +130,30 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const RowTile& t
     for (int s = 0; s < HD / 32; ++s) {
       constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[n][s][k] = (_Float16)(x[s][order[k]] * up);
+      for (int k = 0; k < 8; ++k) q[n][s][k] = (_Float16)(raw_f32<T>(raw[n][s], order[k]) * up);
     }
   }
 }
 
-template <int HD, int NR, bool BF16>
-__global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
+// Waves of a SIMD: what the registers of a variant let live.
+size_t prefix_bytes(int n_tiles) { return ((size_t)(n_tiles + 1) * sizeof(int) + 255) / 256 * 256; }
+
+constexpr int live_waves(int hd_nr) { return hd_nr <= 64 ? 3 : hd_nr <= 256 ? 2 : 1; }
+constexpr int depth(int hd_nr) { return hd_nr <= 128 ? 3 : 2; }
+
+template <int HD, int NR, bool BF16, bool SPLIT>
+__global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(AttnArgs a) {
   constexpr int CT = HD / 16;  // channel tiles; a lane's channels are m * CT .. and, of the result, (4 g + i) * CT ..
   constexpr int kPitch = HD + 4;
   __shared__ float lds_o[kWaves][16][kPitch];
   __shared__ float lds_m[kWaves][16 * NR], lds_l[kWaves][16 * NR];
-  const RowTile t = row_tile(a, (int)blockIdx.x);
-  if (t.row0 >= t.rows) return;
-  const KvSpan span = kv_span(a, t);
-  const int part = (int)blockIdx.z;
-  if (part >= max(span.parts, 1)) return;
-  const int head = (int)blockIdx.y;
-  const int begin = span.begin + part * span.chunk, end = min(span.end, begin + span.chunk);
+  __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
-
-  h8 q[NR][HD / 32];
-  float scale[NR];
-  load_queries<HD, NR, BF16>(a, t, head, q, scale);
+  for_pieces<SPLIT>(a, lds_prefix, [&](const RowTile& t, int head, int begin, int end, int part) {
+  const int lane = fresh_lane(), g = lane >> 4, m = lane & 15;
+  using T = typename std::conditional<BF16, Bf16, F16>::type;
+  uint4 raw[NR][HD / 32];
+  load_queries<HD, NR, T>(a, t, head, lane, raw);
   int lo[NR], hi[NR], all_lo, all_hi, unused;
 #pragma unroll
   for (int n = 0; n < NR; ++n) row_range(a, t, t.row0 + 16 * n + m, lo[n], hi[n]);
@@ -149,6 +162,7 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
   row_range(a, t, min(t.row0 + 16 * NR, t.rows) - 1, all_lo, unused);
 
   Loader<HD> in;
+  in.lane = lane;
   const int page = 1 << a.c.page_log2;
   in.row_bytes = a.c.head_dim / 2;
   in.codes = a.c.codes + (int64_t)head * page * in.row_bytes;
@@ -171,6 +185,21 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
   in.v_at = m * (HD / 32) < in.row_bytes ? m * (HD / 32) : 0;
   in.v_group = min(m * CT / 128, a.c.n_groups - 1) * page;
 
+  constexpr int kStride = kWaves * kStep;
+  constexpr int D = depth(HD * NR);  // steps whose codes are in registers: the one in use and those on their way
+  const int first = begin + wave * kStep;
+  const int steps = first < end ? (end - first + kStride - 1) / kStride : 0;
+  Stage<HD> stage[D];
+#pragma unroll
+  for (int k = 0; k < D - 1; ++k)
+    if (k < steps) {
+      if (k == 0) in.pages(first, kStride, end);
+      in.load(stage[k], k, first + k * kStride);
+    }
+  h8 q[NR][HD / 32];
+  float scale[NR];
+  convert_queries<HD, NR, BF16, T>(a, t, lane, raw, q, scale);
+
   f32x4 o[NR][CT];
   float top[NR], sum[NR];  // the reference of a row's numerators, and their sum in this lane
   uint32_t poisoned[NR];  // groups (bits) whose values a row has seen a NaN in
@@ -183,9 +212,7 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
     for (int c = 0; c < CT; ++c) o[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  constexpr int kStride = kWaves * kStep;
-  const int first = begin + wave * kStep;
-  const int steps = first < end ? (end - first + kStride - 1) / kStride : 0;
+  const uint32_t e = code_exponent();
   // 32 tokens from t0 on
   const auto take = [&](Stage<HD>& now, int t0) {
     // ---- scores
@@ -198,17 +225,17 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
       for (int n = 0; n < NR; ++n) s[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
-        const h8 k = token_codes(now.k[h][c], step, offset);
+        const h8 k = token_codes(now.k[h][c], e, step, offset);
 #pragma unroll
         for (int n = 0; n < NR; ++n) s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][c], s[n][h], 0, 0, 0);
       }
     }
     const bool whole = t0 >= all_lo && t0 + kStep <= all_hi && t0 + kStep <= end && now.there[0] && now.there[1];
     // ---- values that are not finite: out of the products, noted for the rows that see them
-    uint32_t bad = 0;
+    h2 zeros = as_h2(0);  // stays so where all of them are finite
 #pragma unroll
-    for (int j = 0; j < 8; ++j) bad |= ((now.vp[j] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
-    if (__any(bad != 0)) {
+    for (int j = 0; j < 8; ++j) zeros = __builtin_elementwise_fma(as_h2(now.vp[j]), as_h2(0), zeros);
+    if (__any((as_u32(zeros) & 0x7FFF7FFFu) != 0)) {
       int mine = 0;  // which of the lane's tokens, in the group of the lane's channels
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -281,10 +308,10 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t u = __builtin_amdgcn_perm(now.v[2 * j + 1][b / 2], now.v[2 * j][b / 2], b & 1 ? 0x07060302 : 0x05040100);
-        v[0][j] = low_codes(u, step[j], offset[j]);
-        v[1][j] = high_codes(u, step[j], offset[j]);
-        v[2][j] = low_codes(u >> 8, step[j], offset[j]);
-        v[3][j] = high_codes(u >> 8, step[j], offset[j]);
+        v[0][j] = low_codes(u, e, step[j], offset[j]);
+        v[1][j] = high_codes(u, e, step[j], offset[j]);
+        v[2][j] = low_codes(u >> 8, e, step[j], offset[j]);
+        v[3][j] = high_codes(u >> 8, e, step[j], offset[j]);
       }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -294,21 +321,17 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
       }
     }
   };
-  Stage<HD> even, odd;
-  if (steps > 0) {
-    in.pages(first, kStride, end);
-    in.load(even, 0, first);
-  }
-  for (int i = 0; i < steps; i += 2) {
-    const int t0 = first + i * kStride;
-    if (i + 1 < steps) in.load(odd, (i + 1) & 31, t0 + kStride);
-    take(even, t0);
-    if (i + 1 >= steps) break;
-    if (i + 2 < steps) {
-      if (((i + 2) & 31) == 0) in.pages(t0 + 2 * kStride, kStride, end);
-      in.load(even, (i + 2) & 31, t0 + 2 * kStride);
+  for (int i = 0; i < steps; i += D) {
+#pragma unroll
+    for (int k = 0; k < D; ++k) {
+      if (i + k >= steps) break;
+      const int ahead = i + k + D - 1;
+      if (ahead < steps) {
+        if ((ahead & 31) == 0) in.pages(first + ahead * kStride, kStride, end);
+        in.load(stage[(k + D - 1) % D], ahead & 31, first + ahead * kStride);
+      }
+      take(stage[k], first + (i + k) * kStride);
     }
-    take(odd, t0 + kStride);
   }
 
   // ---- the waves join
@@ -321,7 +344,6 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
       lds_l[wave][16 * n + m] = sum[n];
     }
   }
-  const int64_t all_rows = a.n_tokens * a.n_heads;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     if (n) __syncthreads();
@@ -345,13 +367,14 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
         f[w] = __builtin_amdgcn_exp2f(lds_m[w][16 * n + row] - most);
         total = fmaf(f[w], lds_l[w][16 * n + row], total);
       }
-      const int token = r / a.group, of = head * a.group + (r - token * a.group);
-      const int64_t at = (t.token0 + token) * a.n_heads + of;
-      const bool final = span.parts <= 1;
+      const int token = a.by_group.of(r), of = head * a.group + (r - token * a.group);
+      const int64_t at = (int64_t)(t.token0 + token) * a.n_heads + of;
+      const bool final = part < 0;
+      const int64_t slot = (int64_t)part * a.tile_rows + 16 * n + row;
       const float inv = final ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
       if ((int)threadIdx.x % kRowThreads == 0) {
         if (!final) {
-          float* ml = a.part_ml + 2 * (part * all_rows + at);
+          float* ml = a.part_ml + 2 * slot;
           ml[0] = most;
           ml[1] = total;
         } else if (a.lse) {
@@ -365,92 +388,135 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(AttnArgs a) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[k] = fmaf(f[w], lds_o[w][row][c + k], y[k]);
         if (!final) {
-          *reinterpret_cast<f32x4*>(a.part_o + (part * all_rows + at) * a.c.head_dim + c) = f32x4{y[0], y[1], y[2], y[3]};
+          *reinterpret_cast<f32x4*>(a.part_o + slot * a.c.head_dim + c) = f32x4{y[0], y[1], y[2], y[3]};
           continue;
         }
-        const int64_t to = (t.token0 + token) * a.out.ld + (int64_t)of * a.out.ld_head + c;
+        const int64_t to = (int64_t)(t.token0 + token) * a.out.ld + (int64_t)of * a.out.ld_head + c;
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] *= inv;
         store4<BF16>(a, to, y);
       }
     }
-  }
+  }  });
 }
 
-// Joins the parts of rows whose cached tokens several blocks have taken. Block (tile, key head, row of the tile); threads:
-// 8 parts at once, 4 channels each.
-template <bool BF16>
+// Joins the parts of rows whose cached tokens several blocks have taken. Block (tile, key head, R rows of the tile). Threads:
+// 8 / R parts of a row at once, 4 channels each (twice: of heads past 128). Bound by latency: the loads of kJoin parts a
+// thread go out together, the first ones before the parts' largest reference is known.
+constexpr int kJoin = 4;
+template <bool BF16, int H, int R>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
-  __shared__ float lds[8][260];
+  constexpr int G = 8 / R;  // groups of 32 threads for a row
+  __shared__ float lds[8][128 * H + 4];
   __shared__ float lds_l[8];
-  const RowTile t = row_tile(a, (int)blockIdx.x);
-  const int r = t.row0 + (int)blockIdx.z;
-  if (t.row0 >= t.rows || r >= t.rows) return;
-  const KvSpan span = kv_span(a, t);
-  if (span.parts <= 1) return;
-  const int head = (int)blockIdx.y, token = r / a.group, of = head * a.group + (r - token * a.group);
-  const int64_t all_rows = a.n_tokens * a.n_heads, at = (t.token0 + token) * a.n_heads + of;
-  float most = kNothing;
-  for (int i = threadIdx.x & 63; i < span.parts; i += 64) most = fmaxf(most, a.part_ml[2 * (i * all_rows + at)]);
-#pragma unroll
-  for (int d = 32; d; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
+  const int tile = (int)blockIdx.x, head = (int)blockIdx.y;
+  const int before = a.prefix[tile], units = a.prefix[tile + 1] - before;
+  const Split split(a.prefix[a.n_tiles] * a.c.n_kv, a.n_blocks);
+  if (units == 0) return;
+  const int first_unit = before * a.c.n_kv + head * units;
+  const int first_block = split.of(first_unit), parts = split.of(first_unit + units - 1) - first_block + 1;
+  if (parts <= 1) return;
+  const RowTile t = row_tile(a, tile);
   const int group = (int)threadIdx.x / 32, lane = (int)threadIdx.x % 32;
-  float y[2][4] = {}, total = 0.f;
-  for (int i = group; i < span.parts; i += 8) {
-    const float* ml = a.part_ml + 2 * (i * all_rows + at);
-    const float f = __builtin_amdgcn_exp2f(ml[0] - most);
-    total = fmaf(f, ml[1], total);
-    const float* o = a.part_o + (i * all_rows + at) * a.c.head_dim;
+  const int row = (int)blockIdx.z * R + group / G, mine = group % G;
+  const int r = t.row0 + row;
+  const bool there = row < a.tile_rows && r < t.rows;  // (as every thread of a row)
+  const int first_part = 2 * first_block + (split.begin(first_block) == first_unit ? 0 : 1);
+  const auto part = [&](int i) { return (int64_t)(i == 0 ? first_part : 2 * (first_block + i)) * a.tile_rows + (there ? row : 0); };
+  f32x4 u[kJoin][H];
+  float2 w[kJoin];
+  const auto load = [&](int first) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = 128 * h + 4 * lane;
-      if (c < a.c.head_dim) {
-        const f32x4 u = *reinterpret_cast<const f32x4*>(o + c);
+    for (int k = 0; k < kJoin; ++k) {
+      const int64_t i = part(min(first + G * k, parts - 1));
+      w[k] = ((const float2*)a.part_ml)[i];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[h][k] = fmaf(f, u[k], y[h][k]);
-      }
+      for (int h = 0; h < H; ++h)
+        u[k][h] = *reinterpret_cast<const f32x4*>(a.part_o + i * a.c.head_dim + (4 * lane + 128 * h < a.c.head_dim ? 4 * lane + 128 * h : 0));
+    }
+  };
+  load(mine);
+  float most = kNothing;
+  for (int i = lane; i < parts; i += 32) most = fmaxf(most, ((const float2*)a.part_ml)[part(i)].x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
+  float y[H][4] = {}, total = 0.f;
+  for (int first = mine; first < parts; first += G * kJoin) {
+    if (first != mine) load(first);
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) {
+      if (first + G * k >= parts) break;
+      const float f = __builtin_amdgcn_exp2f(w[k].x - most);
+      total = fmaf(f, w[k].y, total);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[h][c] = fmaf(f, u[k][h][c], y[h][c]);
     }
   }
+  if constexpr (G > 1) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) lds[group][128 * h + 4 * lane + k] = y[h][k];
-  if (lane == 0) lds_l[group] = total;
-  __syncthreads();
-  const int c = threadIdx.x;
-  total = 0.f;
+      for (int c = 0; c < 4; ++c) lds[group][128 * h + 4 * lane + c] = y[h][c];
+    if (lane == 0) lds_l[group] = total;
+    __syncthreads();
+    if (mine) return;
+    total = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) total += lds_l[i];
-  if (c == 0 && a.lse) a.lse[at] = total == 0.f ? -__builtin_inff() : (most + __log2f(total)) * kLn2;
-  if (c >= a.c.head_dim) return;
-  float z = 0.f;
+    for (int i = 0; i < G; ++i) total += lds_l[group + i];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z += lds[i][c];
-  z = total == 0.f ? 0.f : z / total;
-  const int64_t to = (t.token0 + token) * a.out.ld + (int64_t)of * a.out.ld_head + c;
-  if (a.out_f32) ((float*)a.out.p)[to] = z;
-  else if (BF16) ((Bf16*)a.out.p)[to] = from_f32<Bf16>(z);
-  else ((F16*)a.out.p)[to] = from_f32<F16>(z);
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        y[h][c] = 0.f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) y[h][c] += lds[group + i][128 * h + 4 * lane + c];
+      }
+  }
+  if (!there) return;
+  const int token = a.by_group.of(r), of = head * a.group + (r - token * a.group);
+  if (lane == 0 && a.lse)
+    a.lse[(int64_t)(t.token0 + token) * a.n_heads + of] = total == 0.f ? -__builtin_inff() : (most + __log2f(total)) * kLn2;
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    const int c = 4 * lane + 128 * h;
+    if (c >= a.c.head_dim) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[h][k] *= inv;
+    store4<BF16>(a, (int64_t)(t.token0 + token) * a.out.ld + (int64_t)of * a.out.ld_head + c, y[h]);
+  }
 }
 
-template <int HD, bool BF16>
+template <int HD, int NR, bool BF16>
 void launch_rows(const AttnArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.n_tiles, (unsigned)a.c.n_kv, (unsigned)a.n_chunks);
-  if (a.tile_rows == 16) rows_kernel<HD, 1, BF16><<<grid, kWaves * 64, 0, stream>>>(a);
-  else rows_kernel<HD, 2, BF16><<<grid, kWaves * 64, 0, stream>>>(a);
+  if (a.n_blocks) rows_kernel<HD, NR, BF16, true><<<dim3((unsigned)a.n_blocks), kWaves * 64, 0, stream>>>(a);
+  else rows_kernel<HD, NR, BF16, false><<<dim3((unsigned)a.n_tiles, (unsigned)a.c.n_kv), kWaves * 64, 0, stream>>>(a);
 }
 
 template <bool BF16>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-  if (a.c.head_dim <= 64) launch_rows<64, BF16>(a, stream);
-  else if (a.c.head_dim <= 128) launch_rows<128, BF16>(a, stream);
-  else launch_rows<256, BF16>(a, stream);
+  const bool one = a.tile_rows == 16;
+  if (a.c.head_dim <= 64) one ? launch_rows<64, 1, BF16>(a, stream) : launch_rows<64, 2, BF16>(a, stream);
+  else if (a.c.head_dim <= 128) one ? launch_rows<128, 1, BF16>(a, stream) : launch_rows<128, 2, BF16>(a, stream);
+  else one ? launch_rows<256, 1, BF16>(a, stream) : launch_rows<256, 2, BF16>(a, stream);
   return hipGetLastError();
+}
+
+template <bool BF16, int R>
+void launch_join_rows(const AttnArgs& a, int rows, hipStream_t stream) {
+  const dim3 grid((unsigned)a.n_tiles, (unsigned)a.c.n_kv, (unsigned)((rows + R - 1) / R));
+  if (a.c.head_dim <= 128) join_kernel<BF16, 1, R><<<grid, 256, 0, stream>>>(a);
+  else join_kernel<BF16, 2, R><<<grid, 256, 0, stream>>>(a);
 }
 
 template <bool BF16>
 hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
-  join_kernel<BF16><<<dim3((unsigned)a.n_tiles, (unsigned)a.c.n_kv, (unsigned)a.tile_rows), 256, 0, stream>>>(a);
+  const int rows = a.q_offsets ? a.tile_rows : min(a.tile_rows, a.each * a.group);
+  // many parts of few rows: all of a block's threads for one row; few parts of many: 32 of them
+  if ((int64_t)a.n_tiles * a.c.n_kv * 8 <= a.n_blocks) launch_join_rows<BF16, 1>(a, rows, stream);
+  else launch_join_rows<BF16, 8>(a, rows, stream);
   return hipGetLastError();
 }
 
@@ -462,24 +528,32 @@ constexpr int kFewRows = 64;
 size_t plan_attention(AttnArgs* a, bool ragged) {
   const int64_t rows_each = (a->n_tokens + a->n_seqs - 1) / a->n_seqs * a->group;
   a->tile_rows = rows_each <= 16 ? 16 : rows_each <= kFewRows ? 32 : prompt_rows(a->c.head_dim);
+  a->tile_log2 = __builtin_ctz((unsigned)a->tile_rows);
+  a->by_group = Divisor((uint32_t)a->group);
+  a->by_kv = Divisor((uint32_t)a->c.n_kv);
+  a->by_tiles = Divisor((uint32_t)((rows_each + a->tile_rows - 1) / a->tile_rows));
   if (ragged) a->n_tiles = (int)(a->n_tokens * a->group / a->tile_rows + a->n_seqs);
   else a->n_tiles = (int)(a->n_seqs * ((rows_each + a->tile_rows - 1) / a->tile_rows));
   int64_t span = a->max_kv;
   if (a->window && a->causal) span = min(span, (int64_t)a->window + a->tile_rows / a->group + kAlign);
-  constexpr int64_t kBlocks = 1024, kLeast = 256;
-  const int64_t blocks = (int64_t)a->n_tiles * a->c.n_kv;
-  int64_t chunks = max((int64_t)1, min(kBlocks / blocks, span / kLeast));
-  a->chunk = (int)(((span + chunks - 1) / chunks + kWaves * kStep - 1) / (kWaves * kStep) * (kWaves * kStep));
-  a->chunk = max(a->chunk, kWaves * kStep);
-  chunks = max((int64_t)1, (span + a->chunk - 1) / a->chunk);
-  a->n_chunks = (int)chunks;
-  if (chunks == 1) return 0;
-  return (size_t)chunks * (size_t)a->n_tokens * a->n_heads * (a->c.head_dim + 2);
+  const int hd = a->c.head_dim <= 64 ? 64 : a->c.head_dim <= 128 ? 128 : 256;
+  const int64_t live = a->tile_rows > 32 ? 1 : live_waves(hd * a->tile_rows / 16);
+  const int64_t units = (int64_t)a->n_tiles * a->c.n_kv * ((span + kUnit - 1) / kUnit);
+  a->n_blocks = (int)min(256 * live, units / kLeastUnits);
+  if (a->n_tiles > kMostTiles || (int64_t)a->n_tiles * a->c.n_kv >= 4 * 256 * live || span <= kLeastUnits * kUnit) a->n_blocks = 0;
+  if (a->n_blocks == 0) return 0;
+  return prefix_bytes(a->n_tiles) + (size_t)2 * a->n_blocks * a->tile_rows * (a->c.head_dim + 2) * sizeof(float);
+}
+
+void place_workspace(AttnArgs* a, void* workspace) {
+  a->prefix = (int*)workspace;
+  a->part_o = (float*)((char*)workspace + prefix_bytes(a->n_tiles));
+  a->part_ml = a->part_o + (size_t)2 * a->n_blocks * a->tile_rows * a->c.head_dim;
 }
 
 hipError_t launch_kv4_attention(const AttnArgs& a, bool bf16, hipStream_t stream) {
   hipError_t e = a.tile_rows > 32 ? launch_kv4_prompt(a, bf16, stream) : bf16 ? launch<true>(a, stream) : launch<false>(a, stream);
-  if (e != hipSuccess || a.n_chunks == 1) return e;
+  if (e != hipSuccess || a.n_blocks == 0) return e;
   return bf16 ? launch_join<true>(a, stream) : launch_join<false>(a, stream);
 }
 

@@ -17,7 +17,7 @@ constexpr int kAlign = 32;  // cached tokens are taken in aligned runs of this m
 // Rows of one key head: row r of a sequence is its new token r / group and query head r % group of the key head's.
 struct RowTile {
   int seq, row0, rows;      // first row of the tile, rows of the sequence (rows <= row0: nothing to do)
-  int64_t token0;           // the sequence's first new token
+  int token0;               // the sequence's first new token
   int kv_len, shift;        // new token i stands at i + shift
 };
 
@@ -30,21 +30,21 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs& a, int tile) {
     int lo = 0, hi = a.n_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)a.q_offsets[mid] * a.group / a.tile_rows + mid <= tile) lo = mid;
+      if (((int64_t)a.q_offsets[mid] * a.group >> a.tile_log2) + mid <= tile) lo = mid;
       else hi = mid - 1;
     }
     r.seq = lo;
     const int64_t begin = min(max((int64_t)a.q_offsets[lo], (int64_t)0), a.n_tokens);
     const int64_t end = min(max((int64_t)a.q_offsets[lo + 1], begin), a.n_tokens);
-    r.token0 = begin;
+    r.token0 = (int)begin;
     q_len = (int)(end - begin);
-    const int64_t first = (int64_t)a.q_offsets[lo] * a.group / a.tile_rows + lo;
-    local = first <= tile && tile - first <= 0x7FFFFFFF / a.tile_rows ? (int)(tile - first) : -1;
+    const int64_t first = ((int64_t)a.q_offsets[lo] * a.group >> a.tile_log2) + lo;
+    local = first <= tile && tile - first <= 0x7FFFFFFF >> a.tile_log2 ? (int)(tile - first) : -1;
   } else {
-    const int tiles = (a.each * a.group + a.tile_rows - 1) / a.tile_rows;
-    r.seq = tile / tiles;
+    const int tiles = (a.each * a.group + a.tile_rows - 1) >> a.tile_log2;
+    r.seq = a.by_tiles.of(tile);
     local = tile - r.seq * tiles;
-    r.token0 = (int64_t)r.seq * a.each;
+    r.token0 = r.seq * a.each;
     q_len = a.each;
   }
   r.rows = local < 0 ? 0 : q_len * a.group;  // a tile before the first sequence's rows has none
@@ -56,27 +56,146 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs& a, int tile) {
 
 // The cached tokens that row r sees: [lo, hi).
 __device__ __forceinline__ void row_range(const AttnArgs& a, const RowTile& t, int r, int& lo, int& hi) {
-  const int p = t.shift + r / a.group;
+  const int p = t.shift + a.by_group.of(r);
   hi = r < t.rows ? (a.causal ? min(t.kv_len, p + 1) : t.kv_len) : 0;
   lo = a.window ? max(0, p - a.window + 1) : 0;
 }
 
-// The cached tokens that a tile's rows see together, and their blocks' share: at least a.chunk, and more where the caller's
-// idea of the longest sequence was too short for a.n_chunks blocks.
+// The cached tokens that a tile's rows see together: [begin, end), in units of kUnit tokens. A tile whose rows see nothing is one
+// unit (its results have to be written), one without rows none.
 struct KvSpan {
-  int begin, end, chunk, parts;
+  int begin, end, units;
 };
 __device__ __forceinline__ KvSpan kv_span(const AttnArgs& a, const RowTile& t) {
-  KvSpan s;
+  KvSpan s = {0, 0, 0};
+  if (t.row0 >= t.rows) return s;
   const int last = min(t.row0 + a.tile_rows, t.rows) - 1;
   int unused;
   row_range(a, t, t.row0, s.begin, unused);
   row_range(a, t, last, unused, s.end);
   s.begin = s.begin / kAlign * kAlign;
-  const int n = max(0, s.end - s.begin);
-  s.chunk = max(a.chunk, ((n + a.n_chunks - 1) / a.n_chunks + kAlign - 1) / kAlign * kAlign);
-  s.parts = (n + s.chunk - 1) / s.chunk;
+  s.units = max(1, (max(0, s.end - s.begin) + kUnit - 1) / kUnit);
   return s;
+}
+
+// The even split. The units of all tiles and key heads (tile by tile, a tile's key heads one after the other) are laid end to
+// end, and each of n_blocks blocks (fewer where a block would get less than kLeastUnits) takes an equal run of them, whatever
+// the sequences' lengths: the end of one tile's tokens, whole tiles, the beginning of another's. What a block has of a
+// tile that it does not have whole goes to its part 2 b (the run begins in it) or 2 b + 1 (the run ends in it), and
+// join_kernel puts the parts together.
+constexpr int kMostTiles = 1024;  // of a split: each block sums up their units
+constexpr int kLeastUnits = 2;
+
+struct Split {
+  int total, blocks, each, more;  // units; the first `more` blocks have each + 1, the others each
+  __device__ __forceinline__ Split(int units, int n_blocks) : total(units) {
+    blocks = max(1, min(units / kLeastUnits, n_blocks));
+    each = (int)((uint32_t)units / (uint32_t)blocks);
+    more = units - each * blocks;
+  }
+  __device__ __forceinline__ int begin(int block) const { return block * each + min(block, more); }
+  __device__ __forceinline__ int of(int unit) const {
+    const int edge = more * (each + 1);
+    return unit < edge ? (int)((uint32_t)unit / (uint32_t)(each + 1)) : more + (int)((uint32_t)(unit - edge) / (uint32_t)max(each, 1));
+  }
+};
+
+// lds: [0 .. n_tiles] the units before each tile (one key head's), then room for the waves' sums; by the 256 threads of a block.
+constexpr int kPrefixInts = kMostTiles + 1 + 4;
+// t, s: the tile of the last one that the thread counted.
+__device__ __forceinline__ void unit_prefix(const AttnArgs& a, int* lds, RowTile& t, KvSpan& s) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  int* const waves = lds + kMostTiles + 1;
+  int before = 0;
+#pragma unroll 1
+  for (int first = 0; first < a.n_tiles; first += 256) {
+    const int tile = first + tid;
+    s.units = 0;
+    if (tile < a.n_tiles) {
+      t = row_tile(a, tile);
+      s = kv_span(a, t);
+    }
+    const int n = s.units;
+    int up = n;  // over the lanes up to this one
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(up, d);
+      if (lane >= d) up += v;
+    }
+    if (lane == 63) waves[tid >> 6] = up;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < tid >> 6) up += waves[w];
+      all += waves[w];
+    }
+    if (tile < a.n_tiles) lds[tile] = before + up - n;
+    before += all;
+    __syncthreads();
+  }
+  if (tid == 0) lds[a.n_tiles] = before;
+  __syncthreads();
+}
+
+// Calls take(tile, key head, begin, end, part) for each piece of this block's work; part -1: a tile's whole span.
+template <bool SPLIT, typename F>
+__device__ __forceinline__ void for_pieces(const AttnArgs& a, int* lds, F take) {
+  if constexpr (!SPLIT) {
+    const RowTile t = row_tile(a, a.n_tiles - 1 - (int)blockIdx.x);  // the last tiles of causal rows see the most
+    const KvSpan s = kv_span(a, t);
+    if (s.units) take(t, (int)blockIdx.y, s.begin, s.end, -1);
+  } else {
+    struct Piece {
+      RowTile t;
+      KvSpan s;
+      int tile;
+    };
+    __shared__ Piece found;
+    Piece p;
+    unit_prefix(a, lds, p.t, p.s);
+    const int block = (int)blockIdx.x;
+    if (block == 0)
+      for (int i = threadIdx.x; i <= a.n_tiles; i += 256) a.prefix[i] = lds[i];
+    const Split split(__builtin_amdgcn_readfirstlane(lds[a.n_tiles]) * a.c.n_kv, a.n_blocks);
+    if (block >= split.blocks) return;
+    int u = split.begin(block);
+    const int u_end = split.begin(block + 1), of_head = a.by_kv.of(u);
+    if (u >= u_end) return;
+    // the tile that the first unit is of: its thread writes it down
+    for (p.tile = threadIdx.x; p.tile < a.n_tiles; p.tile += 256)
+      if (lds[p.tile] <= of_head && of_head < lds[p.tile + 1]) {
+        if (a.n_tiles > 256) {
+          p.t = row_tile(a, p.tile);
+          p.s = kv_span(a, p.t);
+        }
+        found = p;
+      }
+    __syncthreads();
+    const auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    p.tile = uniform(found.tile);
+    p.t = {uniform(found.t.seq), uniform(found.t.row0), uniform(found.t.rows), uniform(found.t.token0), uniform(found.t.kv_len),
+           uniform(found.t.shift)};
+    p.s = {uniform(found.s.begin), uniform(found.s.end), uniform(found.s.units)};
+    bool first = true;
+    while (true) {
+      if (p.s.units) {
+        const int at = u - uniform(lds[p.tile]) * a.c.n_kv, units = p.s.units;
+        const int head = uniform((int)((uint32_t)at / (uint32_t)units)), k = at - head * units, n = min(units - k, u_end - u);
+        if (!first) __syncthreads();  // LDS of the piece before
+        take(p.t, head, p.s.begin + k * kUnit, min(p.s.end, p.s.begin + (k + n) * kUnit), n == units ? -1 : 2 * block + (first ? 0 : 1));
+        first = false;
+        u += n;
+        if (u >= u_end) break;
+        if (k + n < units || head + 1 < a.c.n_kv) continue;
+      }
+      ++p.tile;
+      const RowTile t = row_tile(a, p.tile);
+      p.t = {uniform(t.seq), uniform(t.row0), uniform(t.rows), uniform(t.token0), uniform(t.kv_len), uniform(t.shift)};
+      const KvSpan s = kv_span(a, p.t);
+      p.s = {uniform(s.begin), uniform(s.end), uniform(s.units)};
+    }
+  }
 }
 
 __device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, v); }
@@ -88,24 +207,32 @@ __device__ __forceinline__ uint32_t finite_or_nan(uint32_t w) {
 }
 __device__ __forceinline__ bool not_finite(uint32_t w) { return (((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0; }
 
+// float16 1024 twice, in a register: an instruction takes one constant of 32 bits at most, so that masking codes and setting
+// their exponent is one operation with it, two without.
+__device__ __forceinline__ uint32_t code_exponent() {
+  uint32_t e = 0x64006400u;
+  asm("" : "+v"(e));
+  return e;
+}
+
 // Codes of bits 0 - 3 and 4 - 7 of both halves of u as offset + code * step, one rounding. A code under the exponent of
 // 1024 is 1024 + code (bits 0 - 3) or 1024 + 16 code (bits 4 - 7), from which the code itself comes back exactly.
-__device__ __forceinline__ h2 low_codes(uint32_t u, h2 step, h2 offset) {
-  const h2 c = as_h2((u & 0x000F000Fu) | 0x64006400u) + h2{(_Float16)-1024.f, (_Float16)-1024.f};
+__device__ __forceinline__ h2 low_codes(uint32_t u, uint32_t e, h2 step, h2 offset) {
+  const h2 c = as_h2((u & 0x000F000Fu) | e) + h2{(_Float16)-1024.f, (_Float16)-1024.f};
   return __builtin_elementwise_fma(c, step, offset);
 }
-__device__ __forceinline__ h2 high_codes(uint32_t u, h2 step, h2 offset) {
-  const h2 c = __builtin_elementwise_fma(as_h2((u & 0x00F000F0u) | 0x64006400u), h2{(_Float16)0.0625f, (_Float16)0.0625f},
+__device__ __forceinline__ h2 high_codes(uint32_t u, uint32_t e, h2 step, h2 offset) {
+  const h2 c = __builtin_elementwise_fma(as_h2((u & 0x00F000F0u) | e), h2{(_Float16)0.0625f, (_Float16)0.0625f},
                                          h2{(_Float16)-64.f, (_Float16)-64.f});
   return __builtin_elementwise_fma(c, step, offset);
 }
 
 // Eight consecutive channels of one token: a word of codes, in the order of channels 0, 4, 1, 5, 2, 6, 3, 7 (the queries' operand is
 // brought into the same order).
-__device__ __forceinline__ h8 token_codes(uint32_t w, h2 step, h2 offset) {
+__device__ __forceinline__ h8 token_codes(uint32_t w, uint32_t e, h2 step, h2 offset) {
   const uint32_t v = w >> 8;
-  const h2 a = low_codes(w, step, offset), b = high_codes(w, step, offset);
-  const h2 c = low_codes(v, step, offset), d = high_codes(v, step, offset);
+  const h2 a = low_codes(w, e, step, offset), b = high_codes(w, e, step, offset);
+  const h2 c = low_codes(v, e, step, offset), d = high_codes(v, e, step, offset);
   return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
@@ -135,6 +262,13 @@ __device__ __forceinline__ void store4(const AttnArgs& a, int64_t to, const floa
     for (int k = 0; k < 4; ++k) u.v[k] = BF16 ? from_f32<Bf16>(y[k]).v : from_f32<F16>(y[k]).v;
     *reinterpret_cast<Four*>((uint16_t*)a.out.p + to) = u;
   }
+}
+
+// The lane, which the compiler takes as new each time: what hangs on it is not kept in registers around a loop over pieces.
+__device__ __forceinline__ int fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
 }
 
 // max or sum over the four rows of 16 lanes, in every lane

@@ -129,6 +129,7 @@ struct Producer {
   }
   // bad: for each octet (and group) the tokens whose values are not finite, zeros in LDS then; gone: octets on no page
   __device__ __forceinline__ void store(const Source& s, char* stage, uint8_t* bad, uint8_t* gone) {
+    const uint32_t e = code_exponent();
     if (values) {
       uint32_t any = 0;
 #pragma unroll
@@ -153,10 +154,10 @@ struct Producer {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t u = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], b ? 0x07060302 : 0x05040100);
-          v[0][j] = as_u32(low_codes(u, step[j], offset[j]));
-          v[1][j] = as_u32(high_codes(u, step[j], offset[j]));
-          v[2][j] = as_u32(low_codes(u >> 8, step[j], offset[j]));
-          v[3][j] = as_u32(high_codes(u >> 8, step[j], offset[j]));
+          v[0][j] = as_u32(low_codes(u, e, step[j], offset[j]));
+          v[1][j] = as_u32(high_codes(u, e, step[j], offset[j]));
+          v[2][j] = as_u32(low_codes(u >> 8, e, step[j], offset[j]));
+          v[3][j] = as_u32(high_codes(u >> 8, e, step[j], offset[j]));
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -168,7 +169,7 @@ struct Producer {
         const h2 q = as_h2(finite_or_nan(p[i]));
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<h8*>(stage + L::key_at(token[i], piece[i] * 4 + c)) = token_codes(w[4 * i + c], h2{q.x, q.x}, h2{q.y, q.y});
+          *reinterpret_cast<h8*>(stage + L::key_at(token[i], piece[i] * 4 + c)) = token_codes(w[4 * i + c], e, h2{q.x, q.x}, h2{q.y, q.y});
       }
     }
   }
@@ -183,23 +184,17 @@ __device__ __forceinline__ float sum_over_halves(float v) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-template <int HD, int RT, int WAVES, bool BF16>
+template <int HD, int RT, int WAVES, bool BF16, bool SPLIT>
 __global__ __launch_bounds__(WAVES * 64) void prompt_kernel(AttnArgs a) {
   using T = typename std::conditional<BF16, Bf16, F16>::type;
   using L = Tile<HD, WAVES>;
   constexpr int KS = HD / 16, CT = HD / 32, ST = L::kTokens / 32;
   __shared__ __attribute__((aligned(16))) char lds[2][L::kStage];
   __shared__ __attribute__((aligned(16))) uint8_t lds_bad[2][2][16], lds_gone[2][16];
-  // the last tiles of causal rows see the most: they go first
-  const RowTile t = row_tile(a, a.n_tiles - 1 - (int)blockIdx.x);
-  if (t.row0 >= t.rows) return;
-  const KvSpan span = kv_span(a, t);
-  const int part = (int)blockIdx.z;
-  if (part >= max(span.parts, 1)) return;
-  const int head = (int)blockIdx.y;
-  const int begin = span.begin + part * span.chunk, end = min(span.end, begin + span.chunk);
+  __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, half = lane >> 5, m = lane & 31;
+  for_pieces<SPLIT>(a, lds_prefix, [&](const RowTile& t, int head, int begin, int end, int part) {
+  const int lane = fresh_lane(), half = lane >> 5, m = lane & 31;
   const int wave_row = t.row0 + wave * 32 * RT;
 
   const Source src(a, t, head);
@@ -217,8 +212,8 @@ __global__ __launch_bounds__(WAVES * 64) void prompt_kernel(AttnArgs a) {
   for (int n = 0; n < RT; ++n) {
     const int r = wave_row + 32 * n + m;
     const bool there = r < t.rows;
-    const int token = r / a.group, of = r - token * a.group;
-    const T* row = (const T*)a.q.p + (t.token0 + token) * a.q.ld + (int64_t)(head * a.group + of) * a.q.ld_head;
+    const int token = a.by_group.of(r), of = r - token * a.group;
+    const T* row = (const T*)a.q.p + (int64_t)(t.token0 + token) * a.q.ld + (int64_t)(head * a.group + of) * a.q.ld_head;
     row_range(a, t, r, lo[n], hi[n]);
     hi[n] = min(hi[n], end);
     float top = 0.f, nan = 0.f;
@@ -370,8 +365,7 @@ __global__ __launch_bounds__(WAVES * 64) void prompt_kernel(AttnArgs a) {
   }
 
   // ---- results: a lane has channels 32 c + 8 j + 4 half + 0 .. 3 of its rows
-  const int64_t all_rows = a.n_tokens * a.n_heads;
-  const bool final = span.parts <= 1;
+  const bool final = part < 0;
 #pragma unroll
   for (int n = 0; n < RT; ++n) {
     const float total = sum_over_halves(sum[n]);
@@ -379,11 +373,12 @@ __global__ __launch_bounds__(WAVES * 64) void prompt_kernel(AttnArgs a) {
     poisoned[n] = both[0] | both[1];
     const int r = wave_row + 32 * n + m;
     if (r >= t.rows) continue;
-    const int token = r / a.group, of = head * a.group + (r - token * a.group);
-    const int64_t at = (t.token0 + token) * a.n_heads + of;
+    const int token = a.by_group.of(r), of = head * a.group + (r - token * a.group);
+    const int64_t at = (int64_t)(t.token0 + token) * a.n_heads + of;
+    const int64_t slot = (int64_t)part * a.tile_rows + (r - t.row0);
     if (half == 0) {
       if (!final) {
-        float* ml = a.part_ml + 2 * (part * all_rows + at);
+        float* ml = a.part_ml + 2 * slot;
         ml[0] = top[n];
         ml[1] = total;
       } else if (a.lse) {
@@ -402,21 +397,27 @@ __global__ __launch_bounds__(WAVES * 64) void prompt_kernel(AttnArgs a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = fmaf(o[n][c][4 * j + k], inv, nan);
         if (!final) {
-          *reinterpret_cast<f32x4*>(a.part_o + (part * all_rows + at) * a.c.head_dim + channel) = f32x4{y[0], y[1], y[2], y[3]};
+          *reinterpret_cast<f32x4*>(a.part_o + slot * a.c.head_dim + channel) = f32x4{y[0], y[1], y[2], y[3]};
           continue;
         }
-        store4<BF16>(a, (t.token0 + token) * a.out.ld + (int64_t)of * a.out.ld_head + channel, y);
+        store4<BF16>(a, (int64_t)(t.token0 + token) * a.out.ld + (int64_t)of * a.out.ld_head + channel, y);
       }
     }
   }
+  });
 }
 
 template <int HD, int RT, int WAVES>
 void launch(const AttnArgs& a, bool bf16, hipStream_t stream) {
   static_assert(prompt_rows(HD) == 32 * RT * WAVES, "rows of a block");
-  const dim3 grid((unsigned)a.n_tiles, (unsigned)a.c.n_kv, (unsigned)a.n_chunks);
-  if (bf16) prompt_kernel<HD, RT, WAVES, true><<<grid, WAVES * 64, 0, stream>>>(a);
-  else prompt_kernel<HD, RT, WAVES, false><<<grid, WAVES * 64, 0, stream>>>(a);
+  const dim3 grid = a.n_blocks ? dim3((unsigned)a.n_blocks) : dim3((unsigned)a.n_tiles, (unsigned)a.c.n_kv);
+  if (a.n_blocks) {
+    if (bf16) prompt_kernel<HD, RT, WAVES, true, true><<<grid, WAVES * 64, 0, stream>>>(a);
+    else prompt_kernel<HD, RT, WAVES, false, true><<<grid, WAVES * 64, 0, stream>>>(a);
+  } else {
+    if (bf16) prompt_kernel<HD, RT, WAVES, true, false><<<grid, WAVES * 64, 0, stream>>>(a);
+    else prompt_kernel<HD, RT, WAVES, false, false><<<grid, WAVES * 64, 0, stream>>>(a);
+  }
 }
 
 }  // namespace
