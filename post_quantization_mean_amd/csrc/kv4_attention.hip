@@ -235,7 +235,7 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
     h2 zeros = as_h2(0);  // stays so where all of them are finite
 #pragma unroll
     for (int j = 0; j < 8; ++j) zeros = __builtin_elementwise_fma(as_h2(now.vp[j]), as_h2(0), zeros);
-    if (__any((as_u32(zeros) & 0x7FFF7FFFu) != 0)) {
+    if (rare(__any((as_u32(zeros) & 0x7FFF7FFFu) != 0))) {
       int mine = 0;  // which of the lane's tokens, in the group of the lane's channels
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[4 * h + j] = s[n][h][j];
-      if (!whole) {
+      if (rare(!whole)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       most = max_over_rows(most) * scale[n];
       // The numerators are powers from a reference that is set 2^7 below the largest score and moves only when they would
       // pass 2^15: float16 holds them, down to 2^-31 of the largest.
-      if (__any(most > top[n] + 15.f)) {
+      if (rare(__any(most > top[n] + 15.f))) {
         const float higher = fmaxf(most - 7.f, top[n]);
         const float f = __builtin_amdgcn_exp2f(top[n] - higher);
         top[n] = higher;

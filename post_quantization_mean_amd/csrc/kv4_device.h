@@ -100,15 +100,15 @@ struct Split {
   }
 };
 
-// lds: [0 .. n_tiles] the units before each tile (one key head's), then room for the waves' sums; by the 256 threads of a block.
-constexpr int kPrefixInts = kMostTiles + 1 + 4;
+// lds: [0 .. n_tiles] the units before each tile (one key head's), then room for the waves' sums; by the threads of a block (256 or 512).
+constexpr int kPrefixInts = kMostTiles + 1 + 8;
 // t, s: the tile of the last one that the thread counted.
 __device__ __forceinline__ void unit_prefix(const AttnArgs& a, int* lds, RowTile& t, KvSpan& s) {
   const int tid = threadIdx.x, lane = tid & 63;
   int* const waves = lds + kMostTiles + 1;
   int before = 0;
 #pragma unroll 1
-  for (int first = 0; first < a.n_tiles; first += 256) {
+  for (int first = 0; first < a.n_tiles; first += blockDim.x) {
     const int tile = first + tid;
     s.units = 0;
     if (tile < a.n_tiles) {
@@ -125,8 +125,7 @@ __device__ __forceinline__ void unit_prefix(const AttnArgs& a, int* lds, RowTile
     if (lane == 63) waves[tid >> 6] = up;
     __syncthreads();
     int all = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < (int)blockDim.x >> 6; ++w) {
       if (w < tid >> 6) up += waves[w];
       all += waves[w];
     }
@@ -156,16 +155,16 @@ __device__ __forceinline__ void for_pieces(const AttnArgs& a, int* lds, F take) 
     unit_prefix(a, lds, p.t, p.s);
     const int block = (int)blockIdx.x;
     if (block == 0)
-      for (int i = threadIdx.x; i <= a.n_tiles; i += 256) a.prefix[i] = lds[i];
+      for (int i = threadIdx.x; i <= a.n_tiles; i += blockDim.x) a.prefix[i] = lds[i];
     const Split split(__builtin_amdgcn_readfirstlane(lds[a.n_tiles]) * a.c.n_kv, a.n_blocks);
     if (block >= split.blocks) return;
     int u = split.begin(block);
     const int u_end = split.begin(block + 1), of_head = a.by_kv.of(u);
     if (u >= u_end) return;
     // the tile that the first unit is of: its thread writes it down
-    for (p.tile = threadIdx.x; p.tile < a.n_tiles; p.tile += 256)
+    for (p.tile = threadIdx.x; p.tile < a.n_tiles; p.tile += blockDim.x)
       if (lds[p.tile] <= of_head && of_head < lds[p.tile + 1]) {
-        if (a.n_tiles > 256) {
+        if (a.n_tiles > (int)blockDim.x) {
           p.t = row_tile(a, p.tile);
           p.s = kv_span(a, p.t);
         }
@@ -206,6 +205,9 @@ __device__ __forceinline__ uint32_t finite_or_nan(uint32_t w) {
   return (((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u) ? 0x7E007E00u : w;
 }
 __device__ __forceinline__ bool not_finite(uint32_t w) { return (((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0; }
+
+// A branch that is seldom taken: what it needs in other registers is moved there in the branch, not around it.
+__device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
 
 // float16 1024 twice, in a register: an instruction takes one constant of 32 bits at most, so that masking codes and setting
 // their exponent is one operation with it, two without.

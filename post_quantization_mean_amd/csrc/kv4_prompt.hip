@@ -1,14 +1,18 @@
 // Attention over the 4-bit cache with many rows of a key head: prompts.
 //
-// Bound by the matrix units: 4 head_dim operations a row and cached token. A block takes 32 RT rows for each of its waves (a
-// row: one query head of one new token) and goes over the cached tokens in tiles of kTile, whose keys and values its
-// threads turn into float16 in LDS once for all of its rows (1.7 vector operations a code, a quarter of what the softmax
-// needs). The tile two ahead is on its way from memory and the next one is being written while a tile is used: two LDS stages, one
-// barrier a tile. With v_mfma_f32_32x32x16_f16:
+// Bound by the matrix units and the vector units that feed them: 4 head_dim operations a row and cached token, beside one
+// exponential. A block takes 32 rows for each of its waves (a row: one query head of one new token) and goes over the cached
+// tokens in tiles of kTokens, whose keys and values its threads turn into float16 in LDS once for all of its rows (1.7
+// vector operations a code). The tile after the one in use is written to LDS between its products, the one after that is on
+// its way from memory: two LDS stages, one barrier a tile. With v_mfma_f32_32x32x16_f16:
 //   S^T = K Q^T   A: token lane % 32, 8 channels; B: the same channels of row lane % 32; D: tokens 4 h + 8 j + 0 .. 3 of that
 //                 row (h = lane / 32, j = 0 .. 3).
 //   O^T = V^T P^T B is what the softmax left in the lane: tokens 4 h + 0 .. 3 and 8 + 4 h + 0 .. 3 of each 16; values lie in LDS
 //                 by channel, those 8 tokens side by side.
+// A wave's products and its softmax overlap: while the scores of 32 tokens become numerators, the next 32 tokens' scores
+// are multiplied, and while their maximum is found, the 32 before them meet the values. 32 rows a wave, so that two
+// waves of a SIMD fit its registers without the accumulators' moves between its two files: 64 rows a wave, one wave a
+// SIMD, took 2.93 ms instead of 1.78 for 4096 tokens of 64 heads on 8 behind 8192.
 // Rounding: as in kv4_attention.hip.
 #include <type_traits>
 
@@ -21,32 +25,38 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <int HD, int WAVES>
 struct Tile {
-  static constexpr int kTokens = WAVES * 2048 / HD;  // one piece of work for each thread: 64 codes
-  static constexpr int kOctets = kTokens / 8;        // of 8 tokens
-  static constexpr int kKeyRow = HD * 2, kValueRow = kTokens * 2;  // bytes
-  static constexpr int kStage = kTokens * HD * 4;
-  // 16-byte chunk c of a row: spread over the banks by the row
-  static __device__ __forceinline__ int key_at(int token, int c) {
-    constexpr int n = HD / 8;  // chunks of a row
-    return token * kKeyRow + ((c ^ (n >= 16 ? token & 15 : (token >> 1) & 7)) << 4);
-  }
-  static __device__ __forceinline__ int value_at(int channel, int o) {
-    constexpr int n = kOctets;
-    return kTokens * kKeyRow + channel * kValueRow + ((o ^ (n >= 16 ? channel & 15 : n == 8 ? (channel >> 1) & 7 : (channel >> 2) & 3)) << 4);
-  }
-  // first token of an octet's two runs of four (the second one lies 8 further)
-  static __device__ __forceinline__ int octet_token(int o) { return (o >> 1) * 16 + (o & 1) * 4; }
+  static constexpr int kTokens = WAVES * 2048 / HD;  // a thread turns 32 codes of keys and 32 of values
+  static constexpr int kOctets = kTokens / 8, kQuads = kTokens / 4;
+  // Rows of LDS: a token's keys, a channel's values. Sixteen bytes more than they hold, so that sixteen rows' chunks at the same
+  // place lie in different banks and a chunk's place is a constant.
+  static constexpr int kKeyRow = HD * 2 + 16, kValueRow = kTokens * 2 + 16;
+  static constexpr int kValues = kTokens * kKeyRow, kStage = kValues + HD * kValueRow;
+  static __device__ __forceinline__ int key_at(int token, int c) { return token * kKeyRow + c * 16; }
+  // A channel's row: channels 8 i + k lie in rows k HD/8 + i, which the lanes that write them (i) find in different banks, and
+  // which leaves a lane of the result eight channels side by side.
+  static __device__ __forceinline__ int value_row(int channel) { return channel % 8 * (HD / 8) + channel / 8; }
+  // Chunk o of a row: the eight tokens 16 (o / 2) + 4 (o % 2) + 0 .. 3 and 8 + those.
+  static __device__ __forceinline__ int value_at(int row, int o) { return kValues + row * kValueRow + o * 16; }
 };
 
-// What a block needs to fetch its key head's cached tokens.
-struct Source {
-  const uint8_t* codes;
+// A wave's part of turning tiles into float16: the keys and values of kTokens / WAVES consecutive tokens; a lane has 32 channels
+// of one token's keys, and 8 channels of four tokens' values. Sixteen tokens lie on one page, so that addresses are a
+// page's, the wave's, and an offset of the lane's that stays.
+template <int HD, int WAVES>
+struct Producer {
+  using L = Tile<HD, WAVES>;
+  static constexpr int kMine = L::kTokens / WAVES, kRuns = kMine > 16 ? kMine / 16 : 1;  // runs of 16 tokens of a wave
+  const uint8_t* codes;                  // the key head's keys in page 0, and what lies from keys to values
   const uint32_t* params;
   int64_t page_codes, page_params, v_codes, v_params;
   const int32_t* table;
-  int page_log2, page_mask, row_bytes;
+  int page_log2, page_mask, row_bytes, first;  // first: the wave's first token in a tile
   uint32_t n_pages;
-  __device__ __forceinline__ Source(const AttnArgs& a, const RowTile& t, int head) {
+  int id[kRuns], next_id[kRuns];         // pages of the tile on its way, and of the one after it
+  uint32_t k[4], kp, v[4], vp[4];        // codes and params of the tile on its way
+  int k_run, v_run, k_off, kp_off, v_off, vp_off, k_lds, v_lds, flag, gone;
+
+  __device__ __forceinline__ Producer(const AttnArgs& a, const RowTile& t, int head, int wave, int lane) {
     const int page = 1 << a.c.page_log2;
     row_bytes = a.c.head_dim / 2;
     codes = a.c.codes + (int64_t)head * page * row_bytes;
@@ -59,119 +69,105 @@ struct Source {
     page_log2 = a.c.page_log2;
     page_mask = page - 1;
     n_pages = (uint32_t)a.c.n_pages;
-  }
-};
-
-// A thread's part of turning tiles into float16: one octet of tokens of 8 channels of the values, or 2 x 32 channels of
-// tokens of the keys (the waves of a block divide evenly: the choice is uniform in a wave).
-template <int HD, int WAVES>
-struct Producer {
-  using L = Tile<HD, WAVES>;
-  static constexpr int kPieces = HD / 32;  // 32 channels of a token's keys
-  uint32_t w[8], p[8];                     // codes, params of the tile on its way
-  int id[2], next_id[2];                   // its pages, and those of the tile after it
-  bool values;
-  int octet, channels;                     // values
-  int token[2], piece[2];                  // keys
-  int at, group;                           // this thread's bytes of a row (keys: both pieces), params of its group
-  int key_at[2], key_group[2];
-
-  __device__ __forceinline__ Producer(const AttnArgs& a) {
-    const int tid = threadIdx.x, row_bytes = a.c.head_dim / 2, page = 1 << a.c.page_log2;
-    values = __builtin_amdgcn_readfirstlane(tid) < WAVES * 32;
-    octet = tid % L::kOctets;
-    channels = tid / L::kOctets * 8 % HD;
+    first = wave * kMine;
+    const int token = lane / (HD / 32), piece = lane % (HD / 32);
     // channels past the head's last one repeat its first ones: their queries are zeros, their results are not stored
-    at = channels < a.c.head_dim ? channels / 2 : 0;
-    group = min(channels / 128, a.c.n_groups - 1) * page;
+    k_off = token % 16 * row_bytes + (piece * 16 < row_bytes ? piece * 16 : 0);
+    kp_off = min(piece / 4, a.c.n_groups - 1) * page + token % 16;
+    k_lds = L::key_at(first + token, 4 * piece);
+    const int quads = kMine / 4, quad = lane % quads, octet = lane / quads;  // quads 2 o and 2 o + 1 are chunk o
+    const int in_tile = first / 4 + quad, at = in_tile / 2 % 2 * 4 + in_tile % 2 * 8;  // in its run
+    v_off = at * row_bytes + (octet * 4 < row_bytes ? octet * 4 : 0);
+    vp_off = min(octet / 16, a.c.n_groups - 1) * page + at;
+    v_lds = L::value_at(octet, in_tile / 2) + in_tile % 2 * 8;
+    flag = octet % 16 == 0 ? 2 * in_tile + octet / 16 : -1;
+    k_run = kRuns > 1 ? token / 16 : 0;
+    v_run = kRuns > 1 ? quad / 4 : 0;
+    gone = 0;
+  }
+  __device__ __forceinline__ void pages(int t0, int end) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int task = (tid + i * WAVES * 32) % (WAVES * 64);
-      token[i] = task / kPieces;
-      piece[i] = task % kPieces;
-      key_at[i] = piece[i] * 16 < row_bytes ? piece[i] * 16 : 0;
-      key_group[i] = min(piece[i] / 4, a.c.n_groups - 1) * page;
+    for (int i = 0; i < kRuns; ++i) {
+      const int t = t0 + (first & ~15) + 16 * i;
+      next_id[i] = t < end ? table[t >> page_log2] : -1;
     }
   }
-  __device__ __forceinline__ int first_token(int i) const { return values ? L::octet_token(octet) : token[i]; }
-  __device__ __forceinline__ void pages(const Source& s, int t0, int end) {
+  __device__ __forceinline__ bool there(int i) const { return (uint32_t)id[i] < n_pages; }
+  // The lane's page and place in it: offsets of bytes of codes and of words of params.
+  __device__ __forceinline__ void place(int t0, int run, int64_t& c, int64_t& p) const {
+    int in_page = t0 & page_mask;
+    int64_t page = there(0) ? id[0] : 0;
+    c = page * page_codes + (int64_t)in_page * row_bytes;
+    p = page * page_params + in_page;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = t0 + first_token(i);
-      next_id[i] = t < end ? s.table[t >> s.page_log2] : -1;
+    for (int i = 1; i < kRuns; ++i) {
+      in_page = (t0 + 16 * i) & page_mask;
+      page = there(i) ? id[i] : 0;
+      if (run == i) c = page * page_codes + (int64_t)in_page * row_bytes, p = page * page_params + in_page;
     }
   }
-  __device__ __forceinline__ void load(const Source& s, int t0) {
-    id[0] = next_id[0];
-    id[1] = next_id[1];
-    if (values) {
-      const int64_t page = (uint32_t)id[0] < s.n_pages ? id[0] : 0;
-      const int in_page = (t0 + L::octet_token(octet)) & s.page_mask;
-      const uint8_t* c = s.codes + s.v_codes + page * s.page_codes + in_page * s.row_bytes + at;
-      const uint32_t* q = s.params + s.v_params + page * s.page_params + group + in_page;
+  __device__ __forceinline__ void load_keys(int t0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t*>(c + (i / 4 * 8 + i % 4) * s.row_bytes);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 u = *reinterpret_cast<const uint4*>(q + 8 * i);
-        p[4 * i] = u.x, p[4 * i + 1] = u.y, p[4 * i + 2] = u.z, p[4 * i + 3] = u.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t page = (uint32_t)id[i] < s.n_pages ? id[i] : 0;
-        const int in_page = (t0 + token[i]) & s.page_mask;
-        const uint4 u = *reinterpret_cast<const uint4*>(s.codes + page * s.page_codes + in_page * s.row_bytes + key_at[i]);
-        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-        p[i] = s.params[page * s.page_params + key_group[i] + in_page];
-      }
-    }
+    for (int i = 0; i < kRuns; ++i) id[i] = __builtin_amdgcn_readfirstlane(next_id[i]);
+    int64_t c, p;
+    place(t0 + first, k_run, c, p);
+    const uint4 u = *reinterpret_cast<const uint4*>(codes + c + (uint32_t)k_off);
+    k[0] = u.x, k[1] = u.y, k[2] = u.z, k[3] = u.w;
+    kp = params[p + (uint32_t)kp_off];
   }
-  // bad: for each octet (and group) the tokens whose values are not finite, zeros in LDS then; gone: octets on no page
-  __device__ __forceinline__ void store(const Source& s, char* stage, uint8_t* bad, uint8_t* gone) {
-    const uint32_t e = code_exponent();
-    if (values) {
-      uint32_t any = 0;
+  __device__ __forceinline__ void load_values(int t0) {  // after load_keys
+    int64_t c, p;
+    place(t0 + (first & ~15), v_run, c, p);
+    gone = there(0) ? 0 : 16;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) any |= ((p[i] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
-      int tokens = 0;
-      if (any) {
+    for (int i = 1; i < kRuns; ++i)
+      if (v_run == i) gone = there(i) ? 0 : 16;
+    const uint8_t* from = codes + v_codes + c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (not_finite(p[i])) tokens |= 1 << i, p[i] = 0;
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint32_t*>(from + i * row_bytes + (uint32_t)v_off);
+    const uint4 u = *reinterpret_cast<const uint4*>(params + v_params + p + (uint32_t)vp_off);
+    vp[0] = u.x, vp[1] = u.y, vp[2] = u.z, vp[3] = u.w;
+  }
+  // Half of the keys (two words).
+  template <int HALF>
+  __device__ __forceinline__ void store_keys(char* stage, uint32_t e) {
+    const h2 q = as_h2(finite_or_nan(kp));
+#pragma unroll
+    for (int c = 2 * HALF; c < 2 * HALF + 2; ++c)
+      *reinterpret_cast<h8*>(stage + k_lds + 16 * c) = token_codes(k[c], e, h2{q.x, q.x}, h2{q.y, q.y});
+  }
+  // Half of the values (four channels). flags: for each quad, a byte for each group: the tokens whose values are not
+  // finite (bits 0 - 3; zeros in LDS then), and whether they lie on no page (bit 4).
+  template <int HALF>
+  __device__ __forceinline__ void store_values(char* stage, uint8_t* flags, uint32_t e) {
+    if constexpr (HALF == 0) {
+      int bad = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool b = not_finite(vp[i]);
+        bad |= b ? 1 << i : 0;
+        vp[i] = b ? 0 : vp[i];
       }
-      if (channels % 128 == 0) bad[channels / 128 * 16 + octet] = (uint8_t)tokens;
-      if (channels == 0) gone[octet] = (uint32_t)id[0] < s.n_pages ? 0 : 1;
-      h2 step[4], offset[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        step[j] = as_h2(__builtin_amdgcn_perm(p[2 * j + 1], p[2 * j], 0x05040100));
-        offset[j] = as_h2(__builtin_amdgcn_perm(p[2 * j + 1], p[2 * j], 0x07060302));
-      }
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        uint32_t v[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t u = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], b ? 0x07060302 : 0x05040100);
-          v[0][j] = as_u32(low_codes(u, e, step[j], offset[j]));
-          v[1][j] = as_u32(high_codes(u, e, step[j], offset[j]));
-          v[2][j] = as_u32(low_codes(u >> 8, e, step[j], offset[j]));
-          v[3][j] = as_u32(high_codes(u >> 8, e, step[j], offset[j]));
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(stage + L::value_at(channels + 4 * b + c, octet)) = make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const h2 q = as_h2(finite_or_nan(p[i]));
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<h8*>(stage + L::key_at(token[i], piece[i] * 4 + c)) = token_codes(w[4 * i + c], e, h2{q.x, q.x}, h2{q.y, q.y});
+      if (flag >= 0) {
+        flags[flag] = (uint8_t)(bad | gone);
+        if (HD <= 128) flags[flag + 1] = 0;
       }
     }
+    h2 step[2], offset[2];
+    uint32_t f[4][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      step[j] = as_h2(__builtin_amdgcn_perm(vp[2 * j + 1], vp[2 * j], 0x05040100));
+      offset[j] = as_h2(__builtin_amdgcn_perm(vp[2 * j + 1], vp[2 * j], 0x07060302));
+      const uint32_t u = __builtin_amdgcn_perm(v[2 * j + 1], v[2 * j], HALF ? 0x07060302 : 0x05040100);
+      f[0][j] = as_u32(low_codes(u, e, step[j], offset[j]));
+      f[1][j] = as_u32(high_codes(u, e, step[j], offset[j]));
+      f[2][j] = as_u32(low_codes(u >> 8, e, step[j], offset[j]));
+      f[3][j] = as_u32(high_codes(u >> 8, e, step[j], offset[j]));
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint2*>(stage + v_lds + (4 * HALF + c) * (HD / 8) * L::kValueRow) = make_uint2(f[c][0], f[c][1]);
   }
 };
 
@@ -184,248 +180,289 @@ __device__ __forceinline__ float sum_over_halves(float v) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-template <int HD, int RT, int WAVES, bool BF16, bool SPLIT>
-__global__ __launch_bounds__(WAVES * 64) void prompt_kernel(AttnArgs a) {
+template <int HD, int WAVES, bool BF16, bool SPLIT>
+__global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(AttnArgs a) {
   using T = typename std::conditional<BF16, Bf16, F16>::type;
   using L = Tile<HD, WAVES>;
   constexpr int KS = HD / 16, CT = HD / 32, ST = L::kTokens / 32;
+  constexpr bool PIPED = HD <= 128;  // (heads past 128 leave no registers for it)
   __shared__ __attribute__((aligned(16))) char lds[2][L::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds_bad[2][2][16], lds_gone[2][16];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_flags[2][2 * L::kQuads];
   __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   for_pieces<SPLIT>(a, lds_prefix, [&](const RowTile& t, int head, int begin, int end, int part) {
   const int lane = fresh_lane(), half = lane >> 5, m = lane & 31;
-  const int wave_row = t.row0 + wave * 32 * RT;
+  const int r = t.row0 + wave * 32 + m;  // the lane's row
+  const uint32_t e = code_exponent();
 
-  const Source src(a, t, head);
-  Producer<HD, WAVES> in(a);
+  Producer<HD, WAVES> in(a, t, head, wave, lane);
   const int tiles = begin < end ? (end - begin + L::kTokens - 1) / L::kTokens : 0;
-  in.pages(src, begin, end);
-  if (tiles > 0) in.load(src, begin);
-  in.pages(src, begin + L::kTokens, end);
+  in.pages(begin, end);
+  in.load_keys(begin);
+  in.load_values(begin);
+  in.pages(begin + L::kTokens, end);
 
   // ---- this wave's queries
-  h8 q[RT][KS];
-  float scale[RT];
-  int lo[RT], hi[RT];
-#pragma unroll
-  for (int n = 0; n < RT; ++n) {
-    const int r = wave_row + 32 * n + m;
+  h8 q[KS];
+  int lo, hi;
+  row_range(a, t, r, lo, hi);
+  hi = min(hi, end);
+  float scale;
+  {
     const bool there = r < t.rows;
-    const int token = a.by_group.of(r), of = r - token * a.group;
-    const T* row = (const T*)a.q.p + (int64_t)(t.token0 + token) * a.q.ld + (int64_t)(head * a.group + of) * a.q.ld_head;
-    row_range(a, t, r, lo[n], hi[n]);
-    hi[n] = min(hi[n], end);
-    float top = 0.f, nan = 0.f;
+    const int row = min(r, t.rows - 1), token = a.by_group.of(row), of = row - token * a.group;
+    const T* from = (const T*)a.q.p + (int64_t)(t.token0 + token) * a.q.ld + (int64_t)(head * a.group + of) * a.q.ld_head;
+    float largest = 0.f, nan = 0.f;
     uint4 raw[KS];
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const int c = 16 * s + 8 * half;
-      raw[s] = make_uint4(0, 0, 0, 0);
-      if (there && c < a.c.head_dim) raw[s] = __builtin_bit_cast(uint4, *reinterpret_cast<const Chunk<T>*>(row + c));
+      raw[s] = __builtin_bit_cast(uint4, *reinterpret_cast<const Chunk<T>*>(from + (c < a.c.head_dim ? c : 0)));
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if (!there || 16 * s + 8 * half >= a.c.head_dim) raw[s] = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float x = raw_f32<T>(raw[s], k);
-        top = fmaxf(top, fabsf(x));
+        largest = fmaxf(largest, fabsf(x));
         nan = fmaf(x, 0.f, nan);
       }
     }
     float up, down;
-    query_range<BF16>(max_over_halves(top), a.scale, up, down);
-    scale[n] = fmaxf(fabsf(a.scale) * down, 0x1p-126f) + sum_over_halves(nan);
+    query_range<BF16>(max_over_halves(largest), a.scale, up, down);
+    scale = fmaxf(fabsf(a.scale) * down, 0x1p-126f) + sum_over_halves(nan);  // NaN for a row with a NaN or an infinity
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[n][s][k] = (_Float16)(raw_f32<T>(raw[s], order[k]) * up);
+      for (int k = 0; k < 8; ++k) q[s][k] = (_Float16)(raw_f32<T>(raw[s], order[k]) * up);
     }
   }
   // tokens that every row of the wave sees, and that any of them sees
   int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;
+  const int wave_row = t.row0 + wave * 32;
   if (wave_row < t.rows) {
     row_range(a, t, wave_row, any_lo, all_hi);
-    row_range(a, t, min(wave_row + 32 * RT, t.rows) - 1, all_lo, any_hi);
+    row_range(a, t, min(wave_row + 32, t.rows) - 1, all_lo, any_hi);
     all_hi = min(all_hi, end);
     any_hi = min(any_hi, end);
   }
 
-  f32x16 o[RT][CT];
-  float top[RT], sum[RT];
-  uint32_t poisoned[RT];
+  f32x16 o[CT];
+  float top = kNothing, sum = 0.f;
+  uint32_t poisoned = 0;  // groups (bits) whose values the row has seen a NaN in
 #pragma unroll
-  for (int n = 0; n < RT; ++n) {
-    top[n] = kNothing;
-    sum[n] = 0.f;
-    poisoned[n] = 0;
+  for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[n][c][i] = 0.f;
-  }
+    for (int j = 0; j < 16; ++j) o[c][j] = 0.f;
 
-  if (tiles > 0) {
-    in.store(src, lds[0], lds_bad[0][0], lds_gone[0]);
-    if (tiles > 1) {
-      in.load(src, begin + L::kTokens);
-      in.pages(src, begin + 2 * L::kTokens, end);
+  // ---- the steps of 32 tokens of a tile
+  const auto scores = [&](const char* stage, int st) {
+    f32x16 s;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) s[j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8*>(stage + L::key_at(32 * st + m, 2 * k + half)), q[k], s, 0, 0, 0);
+    return s;
+  };
+  // The numerators' reference: 2^7 below the largest score, moved only when a numerator would pass 2^15.
+  const auto refer = [&](const f32x16& s) {
+    float most = s[0];
+#pragma unroll
+    for (int j = 1; j < 16; ++j) most = fmaxf(most, s[j]);
+    most = max_over_halves(most) * scale;
+    if (rare(__any(most > top + 15.f))) {
+      const float higher = fmaxf(most - 7.f, top);
+      const float f = __builtin_amdgcn_exp2f(top - higher);
+      top = higher;
+      sum *= f;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) o[c] *= f;
     }
+  };
+  const auto numerators = [&](const f32x16& s, h8 (&p)[2]) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      // rounded towards zero, and summed as rounded: the weights add up to one, and the rounding's bias cancels
+      const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(fmaf(s[j], scale, -top)),
+                                                  __builtin_amdgcn_exp2f(fmaf(s[j + 1], scale, -top)));
+      const h2 pair = __builtin_bit_cast(h2, two);
+      sum = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum, false);
+      p[j / 8][j % 8] = pair.x;
+      p[j / 8][j % 8 + 1] = pair.y;
+    }
+  };
+  const auto weigh = [&](const char* stage, int st, const h8 (&p)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8*>(stage + L::value_at(32 * c + m, 4 * st + 2 * u + half)), p[u],
+                                                      o[c], 0, 0, 0);
+  };
+  // a quarter of the next tile's way into LDS
+  const auto produce = [&](int quarter, int i, char* stage, uint8_t* flags) {
+    const bool more = i + 2 < tiles;
+    const int t2 = begin + (i + 2) * L::kTokens;
+    if (quarter == 0) in.template store_keys<0>(stage, e);
+    if (quarter == 1) {
+      in.template store_keys<1>(stage, e);
+      if (more) in.load_keys(t2);
+    }
+    if (quarter == 2) in.template store_values<0>(stage, flags, e);
+    if (quarter == 3) {
+      in.template store_values<1>(stage, flags, e);
+      if (more) {
+        in.load_values(t2);
+        in.pages(t2 + L::kTokens, end);
+      }
+    }
+  };
+
+#pragma unroll
+  for (int quarter = 0; quarter < 4; ++quarter)
+    if (tiles > 0) {
+      if (quarter == 0) in.template store_keys<0>(lds[0], e);
+      if (quarter == 1) in.template store_keys<1>(lds[0], e);
+      if (quarter == 2) in.template store_values<0>(lds[0], lds_flags[0], e);
+      if (quarter == 3) in.template store_values<1>(lds[0], lds_flags[0], e);
+    }
+  if (tiles > 1) {
+    in.load_keys(begin + L::kTokens);
+    in.load_values(begin + L::kTokens);
+    in.pages(begin + 2 * L::kTokens, end);
   }
   for (int i = 0; i < tiles; ++i) {
     const int t0 = begin + i * L::kTokens, b = i & 1;
-    char* const stage = lds[b];
+    const char* const stage = lds[b];
+    char* const next = lds[b ^ 1];
+    uint8_t* const next_flags = lds_flags[b ^ 1];
+    const bool follows = i + 1 < tiles;
     __syncthreads();
-    if (i + 1 < tiles) {
-      in.store(src, lds[b ^ 1], lds_bad[b ^ 1][0], lds_gone[b ^ 1]);
-      if (i + 2 < tiles) {
-        in.load(src, t0 + 2 * L::kTokens);
-        in.pages(src, t0 + 3 * L::kTokens, end);
+    const uint32_t flag = lane < L::kQuads / 2 ? reinterpret_cast<const uint32_t*>(lds_flags[b])[lane] : 0;
+    const bool odd = __any(flag != 0);  // pages or values that are not there
+    if (PIPED && t0 >= all_lo && t0 + L::kTokens <= all_hi && !odd) {
+      f32x16 s = scores(stage, 0);
+      h8 p[2];
+#pragma unroll
+      for (int st = 0; st < ST; ++st) {
+        if (st > 0) weigh(stage, st - 1, p);
+        if (follows) {
+#pragma unroll
+          for (int k = 4 * st / ST; k < 4 * (st + 1) / ST; ++k) produce(k, i, next, next_flags);
+        }
+        refer(s);
+        f32x16 s_next;
+        if (st + 1 < ST) s_next = scores(stage, st + 1);
+        numerators(s, p);
+        if (st + 1 < ST) s = s_next;
       }
+      weigh(stage, ST - 1, p);
+      continue;
     }
-    if (t0 >= any_hi || t0 + L::kTokens <= any_lo) continue;
-    const uint4 gone = *reinterpret_cast<const uint4*>(lds_gone[b]);
-    const bool whole = t0 >= all_lo && t0 + L::kTokens <= all_hi &&
-                       (L::kOctets < 8 ? gone.x == 0 : L::kOctets < 16 ? (gone.x | gone.y) == 0 : (gone.x | gone.y | gone.z | gone.w) == 0);
+    // ---- tiles that some of the wave's rows see in part
+    if (follows) {
 #pragma unroll
+      for (int k = 0; k < 4; ++k) produce(k, i, next, next_flags);
+    }
+#pragma unroll 1
     for (int st = 0; st < ST; ++st) {
-      // ---- scores
-      f32x16 s[RT];
+      const int t1 = t0 + 32 * st;
+      if (t1 >= any_hi || t1 + 32 <= any_lo) continue;
+      f32x16 s = scores(stage, st);
+      if (t1 < all_lo || t1 + 32 > all_hi) {
+        asm volatile("");  // a branch, not selects in every step
+        const int from = lo - t1 - 4 * half, to = hi - t1 - 4 * half;
 #pragma unroll
-      for (int n = 0; n < RT; ++n)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s[n][j] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const h8 f = *reinterpret_cast<const h8*>(stage + L::key_at(32 * st + m, 2 * k + half));
-#pragma unroll
-        for (int n = 0; n < RT; ++n) s[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, q[n][k], s[n], 0, 0, 0);
+        for (int j = 0; j < 16; ++j)
+          if (8 * (j / 4) + j % 4 < from || 8 * (j / 4) + j % 4 >= to) s[j] = -__builtin_inff();
       }
-      if (!whole) {
+      if (rare(odd)) {
+        asm volatile("");
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const int at = 32 * st + 4 * half + 8 * (j / 4) + j % 4;
-          const bool gone_j = lds_gone[b][4 * st + 2 * (j / 8) + half] != 0;
-#pragma unroll
-          for (int n = 0; n < RT; ++n)
-            if (t0 + at < lo[n] || t0 + at >= hi[n] || gone_j) s[n][j] = -__builtin_inff();
-        }
-      }
-      // ---- values that are not finite
-      {
-        uint32_t any = *reinterpret_cast<const uint32_t*>(&lds_bad[b][0][4 * st]);
-        if (HD > 128) any |= *reinterpret_cast<const uint32_t*>(&lds_bad[b][1][4 * st]);
-        if (__builtin_amdgcn_readfirstlane((int)any) != 0) {
+          const int at = t1 + 4 * half + 8 * (j / 4) + j % 4;
+          const uint8_t* flags = &lds_flags[b][2 * (8 * st + 4 * (j / 8) + 2 * half + j / 4 % 2)];
+          const bool seen = at >= lo && at < hi && !(flags[0] & 16);
+          if (!seen) s[j] = -__builtin_inff();
 #pragma unroll
           for (int c = 0; c < (HD + 127) / 128; ++c)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int octet = 4 * st + 2 * (j / 8) + half, at = t0 + 32 * st + 4 * half + 8 * (j / 4) + j % 4;
-              const bool hit = c < a.c.n_groups && (lds_bad[b][c][octet] >> (j % 8) & 1) && !lds_gone[b][octet];
-#pragma unroll
-              for (int n = 0; n < RT; ++n)
-                if (hit && at >= lo[n] && at < hi[n]) poisoned[n] |= 1u << c;
-            }
+            if (seen && (flags[c] >> (j % 4) & 1)) poisoned |= 1u << c;
         }
       }
-      // ---- numerators
-      h8 p[RT][2];
-#pragma unroll
-      for (int n = 0; n < RT; ++n) {
-        float most = s[n][0];
-#pragma unroll
-        for (int j = 1; j < 16; ++j) most = fmaxf(most, s[n][j]);
-        most = max_over_halves(most) * scale[n];
-        if (__any(most > top[n] + 15.f)) {
-          const float higher = fmaxf(most - 7.f, top[n]);
-          const float f = __builtin_amdgcn_exp2f(top[n] - higher);
-          top[n] = higher;
-          sum[n] *= f;
-#pragma unroll
-          for (int c = 0; c < CT; ++c) o[n][c] *= f;
-        }
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(fmaf(s[n][j], scale[n], -top[n])),
-                                                      __builtin_amdgcn_exp2f(fmaf(s[n][j + 1], scale[n], -top[n])));
-          const h2 pair = __builtin_bit_cast(h2, two);
-          sum[n] = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum[n], false);
-          p[n][j / 8][j % 8] = pair.x;
-          p[n][j / 8][j % 8 + 1] = pair.y;
-        }
-      }
-      // ---- their product with the values
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const h8 f = *reinterpret_cast<const h8*>(stage + L::value_at(32 * c + m, 4 * st + 2 * u + half));
-#pragma unroll
-          for (int n = 0; n < RT; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, p[n][u], o[n][c], 0, 0, 0);
-        }
+      refer(s);
+      h8 p[2];
+      numerators(s, p);
+      weigh(stage, st, p);
     }
   }
 
-  // ---- results: a lane has channels 32 c + 8 j + 4 half + 0 .. 3 of its rows
+  // ---- results: row 32 c + 8 j + 4 half + k of LDS, register 4 j + k of accumulator c, is eight channels' row (value_row): a
+  // lane has them side by side
   const bool final = part < 0;
-#pragma unroll
-  for (int n = 0; n < RT; ++n) {
-    const float total = sum_over_halves(sum[n]);
-    const auto both = __builtin_amdgcn_permlane32_swap(poisoned[n], poisoned[n], false, false);
-    poisoned[n] = both[0] | both[1];
-    const int r = wave_row + 32 * n + m;
-    if (r >= t.rows) continue;
+  const float total = sum_over_halves(sum);
+  const auto both = __builtin_amdgcn_permlane32_swap(poisoned, poisoned, false, false);
+  poisoned = both[0] | both[1];
+  if (r < t.rows) {
     const int token = a.by_group.of(r), of = head * a.group + (r - token * a.group);
-    const int64_t at = (int64_t)(t.token0 + token) * a.n_heads + of;
     const int64_t slot = (int64_t)part * a.tile_rows + (r - t.row0);
     if (half == 0) {
       if (!final) {
         float* ml = a.part_ml + 2 * slot;
-        ml[0] = top[n];
+        ml[0] = top;
         ml[1] = total;
       } else if (a.lse) {
-        a.lse[at] = total == 0.f ? -__builtin_inff() : (top[n] + __log2f(total)) * kLn2;
+        a.lse[(int64_t)(t.token0 + token) * a.n_heads + of] = total == 0.f ? -__builtin_inff() : (top + __log2f(total)) * kLn2;
       }
     }
     const float inv = final ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
+    constexpr int kOct = HD / 8;  // rows of the channels 8 i + 0
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const float nan = (poisoned[n] >> (c / 4)) & 1 ? __builtin_nanf("") : 0.f;
+    for (int i = 0; i < HD / 16; ++i) {  // the lane's groups of eight channels: row 8 (i / 4) + 4 half + i % 4 of them
+      const int octet = 8 * (i / 4) + 4 * half + i % 4, channel = 8 * octet;
+      if (channel >= a.c.head_dim) continue;
+      const float nan = (poisoned >> (channel / 128)) & 1 ? __builtin_nanf("") : 0.f;
+      float y[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int channel = 32 * c + 8 * j + 4 * half;
-        if (channel >= a.c.head_dim) continue;
-        float y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = fmaf(o[n][c][4 * j + k], inv, nan);
-        if (!final) {
-          *reinterpret_cast<f32x4*>(a.part_o + slot * a.c.head_dim + channel) = f32x4{y[0], y[1], y[2], y[3]};
-          continue;
-        }
-        store4<BF16>(a, (int64_t)(t.token0 + token) * a.out.ld + (int64_t)of * a.out.ld_head + channel, y);
+      for (int k = 0; k < 8; ++k) {
+        const int row = k * kOct + 8 * (i / 4);  // without half and i % 4
+        y[k] = fmaf(o[row / 32][row % 32 / 8 * 4 + i % 4], inv, nan);
       }
+      if (!final) {
+        f32x4* to = reinterpret_cast<f32x4*>(a.part_o + slot * a.c.head_dim + channel);
+        to[0] = f32x4{y[0], y[1], y[2], y[3]};
+        to[1] = f32x4{y[4], y[5], y[6], y[7]};
+        continue;
+      }
+      const int64_t to = (int64_t)(t.token0 + token) * a.out.ld + (int64_t)of * a.out.ld_head + channel;
+      store4<BF16>(a, to, {y[0], y[1], y[2], y[3]});
+      store4<BF16>(a, to + 4, {y[4], y[5], y[6], y[7]});
     }
   }
   });
 }
 
-template <int HD, int RT, int WAVES>
+template <int HD, int WAVES>
 void launch(const AttnArgs& a, bool bf16, hipStream_t stream) {
-  static_assert(prompt_rows(HD) == 32 * RT * WAVES, "rows of a block");
+  static_assert(prompt_rows(HD) == 32 * WAVES, "rows of a block");
   const dim3 grid = a.n_blocks ? dim3((unsigned)a.n_blocks) : dim3((unsigned)a.n_tiles, (unsigned)a.c.n_kv);
   if (a.n_blocks) {
-    if (bf16) prompt_kernel<HD, RT, WAVES, true, true><<<grid, WAVES * 64, 0, stream>>>(a);
-    else prompt_kernel<HD, RT, WAVES, false, true><<<grid, WAVES * 64, 0, stream>>>(a);
+    if (bf16) prompt_kernel<HD, WAVES, true, true><<<grid, WAVES * 64, 0, stream>>>(a);
+    else prompt_kernel<HD, WAVES, false, true><<<grid, WAVES * 64, 0, stream>>>(a);
   } else {
-    if (bf16) prompt_kernel<HD, RT, WAVES, true, false><<<grid, WAVES * 64, 0, stream>>>(a);
-    else prompt_kernel<HD, RT, WAVES, false, false><<<grid, WAVES * 64, 0, stream>>>(a);
+    if (bf16) prompt_kernel<HD, WAVES, true, false><<<grid, WAVES * 64, 0, stream>>>(a);
+    else prompt_kernel<HD, WAVES, false, false><<<grid, WAVES * 64, 0, stream>>>(a);
   }
 }
 
 }  // namespace
 
 hipError_t launch_kv4_prompt(const AttnArgs& a, bool bf16, hipStream_t stream) {
-  if (a.c.head_dim <= 64) launch<64, 2, 4>(a, bf16, stream);
-  else if (a.c.head_dim <= 128) launch<128, 2, 4>(a, bf16, stream);
-  else launch<256, 1, 4>(a, bf16, stream);
+  if (a.c.head_dim <= 64) launch<64, 8>(a, bf16, stream);
+  else if (a.c.head_dim <= 128) launch<128, 8>(a, bf16, stream);
+  else launch<256, 4>(a, bf16, stream);
   return hipGetLastError();
 }
 
