@@ -273,10 +273,11 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmaxf(most, x[j]);
-      most = max_over_rows(most) * scale[n];
+      most *= scale[n];
       // The numerators are powers from a reference that is set 2^7 below the largest score and moves only when they would
       // pass 2^15: float16 holds them, down to 2^-31 of the largest.
       if (rare(__any(most > top[n] + 15.f))) {
+        most = max_over_rows(most);
         const float higher = fmaxf(most - 7.f, top[n]);
         const float f = __builtin_amdgcn_exp2f(top[n] - higher);
         top[n] = higher;

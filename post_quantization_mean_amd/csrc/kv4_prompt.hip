@@ -26,7 +26,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 template <int HD, int WAVES>
 struct Tile {
   static constexpr int kTokens = WAVES * 2048 / HD;  // a thread turns 32 codes of keys and 32 of values
-  static constexpr int kOctets = kTokens / 8, kQuads = kTokens / 4;
+  static constexpr int kQuads = kTokens / 4, kFlags = (HD + 127) / 128 * kQuads;
   // Rows of LDS: a token's keys, a channel's values. Sixteen bytes more than they hold, so that sixteen rows' chunks at the same
   // place lie in different banks and a chunk's place is a constant.
   static constexpr int kKeyRow = HD * 2 + 16, kValueRow = kTokens * 2 + 16;
@@ -80,7 +80,7 @@ struct Producer {
     v_off = at * row_bytes + (octet * 4 < row_bytes ? octet * 4 : 0);
     vp_off = min(octet / 16, a.c.n_groups - 1) * page + at;
     v_lds = L::value_at(octet, in_tile / 2) + in_tile % 2 * 8;
-    flag = octet % 16 == 0 ? 2 * in_tile + octet / 16 : -1;
+    flag = octet / 16 * L::kQuads + in_tile;  // (the lanes of a group's channels write the same)
     k_run = kRuns > 1 ? token / 16 : 0;
     v_run = kRuns > 1 ? quad / 4 : 0;
     gone = 0;
@@ -136,7 +136,7 @@ struct Producer {
     for (int c = 2 * HALF; c < 2 * HALF + 2; ++c)
       *reinterpret_cast<h8*>(stage + k_lds + 16 * c) = token_codes(k[c], e, h2{q.x, q.x}, h2{q.y, q.y});
   }
-  // Half of the values (four channels). flags: for each quad, a byte for each group: the tokens whose values are not
+  // Half of the values (four channels). flags: for each group and quad a byte: the tokens whose values are not
   // finite (bits 0 - 3; zeros in LDS then), and whether they lie on no page (bit 4).
   template <int HALF>
   __device__ __forceinline__ void store_values(char* stage, uint8_t* flags, uint32_t e) {
@@ -148,10 +148,7 @@ struct Producer {
         bad |= b ? 1 << i : 0;
         vp[i] = b ? 0 : vp[i];
       }
-      if (flag >= 0) {
-        flags[flag] = (uint8_t)(bad | gone);
-        if (HD <= 128) flags[flag + 1] = 0;
-      }
+      flags[flag] = (uint8_t)(bad | gone);
     }
     h2 step[2], offset[2];
     uint32_t f[4][2];
@@ -187,7 +184,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
   constexpr int KS = HD / 16, CT = HD / 32, ST = L::kTokens / 32;
   constexpr bool PIPED = HD <= 128;  // (heads past 128 leave no registers for it)
   __shared__ __attribute__((aligned(16))) char lds[2][L::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds_flags[2][2 * L::kQuads];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_flags[2][L::kFlags];
   __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   for_pieces<SPLIT>(a, lds_prefix, [&](const RowTile& t, int head, int begin, int end, int part) {
@@ -212,7 +209,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
     const bool there = r < t.rows;
     const int row = min(r, t.rows - 1), token = a.by_group.of(row), of = row - token * a.group;
     const T* from = (const T*)a.q.p + (int64_t)(t.token0 + token) * a.q.ld + (int64_t)(head * a.group + of) * a.q.ld_head;
-    float largest = 0.f, nan = 0.f;
+    float size = 0.f, nan = 0.f;
     uint4 raw[KS];
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -225,12 +222,12 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float x = raw_f32<T>(raw[s], k);
-        largest = fmaxf(largest, fabsf(x));
+        size = fmaxf(size, fabsf(x));
         nan = fmaf(x, 0.f, nan);
       }
     }
     float up, down;
-    query_range<BF16>(max_over_halves(largest), a.scale, up, down);
+    query_range<BF16>(max_over_halves(size), a.scale, up, down);
     scale = fmaxf(fabsf(a.scale) * down, 0x1p-126f) + sum_over_halves(nan);  // NaN for a row with a NaN or an infinity
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -258,22 +255,23 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
     for (int j = 0; j < 16; ++j) o[c][j] = 0.f;
 
   // ---- the steps of 32 tokens of a tile
+  const auto key = [&](const char* stage, int st, int k) { return *reinterpret_cast<const h8*>(stage + L::key_at(32 * st + m, 2 * k + half)); };
+  const auto value = [&](const char* stage, int st, int j) {  // j: channel tile j % CT of the sixteen tokens j / CT
+    return *reinterpret_cast<const h8*>(stage + L::value_at(32 * (j % CT) + m, 4 * st + 2 * (j / CT) + half));
+  };
   const auto scores = [&](const char* stage, int st) {
     f32x16 s;
 #pragma unroll
     for (int j = 0; j < 16; ++j) s[j] = 0.f;
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8*>(stage + L::key_at(32 * st + m, 2 * k + half)), q[k], s, 0, 0, 0);
+    for (int k = 0; k < KS; ++k) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(key(stage, st, k), q[k], s, 0, 0, 0);
     return s;
   };
   // The numerators' reference: 2^7 below the largest score, moved only when a numerator would pass 2^15.
-  const auto refer = [&](const f32x16& s) {
-    float most = s[0];
-#pragma unroll
-    for (int j = 1; j < 16; ++j) most = fmaxf(most, s[j]);
-    most = max_over_halves(most) * scale;
+  const auto refer = [&](float most) {
+    most *= scale;
     if (rare(__any(most > top + 15.f))) {
+      most = max_over_halves(most);
       const float higher = fmaxf(most - 7.f, top);
       const float f = __builtin_amdgcn_exp2f(top - higher);
       top = higher;
@@ -282,91 +280,108 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
       for (int c = 0; c < CT; ++c) o[c] *= f;
     }
   };
-  const auto numerators = [&](const f32x16& s, h8 (&p)[2]) {
+  const auto largest = [](const f32x16& s) {
+    float most = s[0];
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      // rounded towards zero, and summed as rounded: the weights add up to one, and the rounding's bias cancels
-      const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(fmaf(s[j], scale, -top)),
-                                                  __builtin_amdgcn_exp2f(fmaf(s[j + 1], scale, -top)));
-      const h2 pair = __builtin_bit_cast(h2, two);
-      sum = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum, false);
-      p[j / 8][j % 8] = pair.x;
-      p[j / 8][j % 8 + 1] = pair.y;
-    }
+    for (int j = 1; j < 16; ++j) most = fmaxf(most, s[j]);
+    return most;
   };
-  const auto weigh = [&](const char* stage, int st, const h8 (&p)[2]) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-        o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8*>(stage + L::value_at(32 * c + m, 4 * st + 2 * u + half)), p[u],
-                                                      o[c], 0, 0, 0);
+  // two of a lane's sixteen numerators
+  const auto numerators = [&](const f32x16& s, int j, h8 (&p)[2]) {
+    // rounded towards zero, and summed as rounded: the weights add up to one, and the rounding's bias cancels
+    const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(fmaf(s[j], scale, -top)),
+                                                __builtin_amdgcn_exp2f(fmaf(s[j + 1], scale, -top)));
+    const h2 pair = __builtin_bit_cast(h2, two);
+    sum = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum, false);
+    p[j / 8][j % 8] = pair.x;
+    p[j / 8][j % 8 + 1] = pair.y;
   };
-  // a quarter of the next tile's way into LDS
+  // A quarter of tile i + 1's way into LDS; the loads of tile i + 2. (Past the last tile: of page 0, into a stage that nobody
+  // reads.)
   const auto produce = [&](int quarter, int i, char* stage, uint8_t* flags) {
-    const bool more = i + 2 < tiles;
     const int t2 = begin + (i + 2) * L::kTokens;
     if (quarter == 0) in.template store_keys<0>(stage, e);
     if (quarter == 1) {
       in.template store_keys<1>(stage, e);
-      if (more) in.load_keys(t2);
+      in.load_keys(t2);
     }
     if (quarter == 2) in.template store_values<0>(stage, flags, e);
     if (quarter == 3) {
       in.template store_values<1>(stage, flags, e);
-      if (more) {
-        in.load_values(t2);
-        in.pages(t2 + L::kTokens, end);
-      }
+      in.load_values(t2);
+      in.pages(t2 + L::kTokens, end);
     }
   };
 
 #pragma unroll
-  for (int quarter = 0; quarter < 4; ++quarter)
-    if (tiles > 0) {
-      if (quarter == 0) in.template store_keys<0>(lds[0], e);
-      if (quarter == 1) in.template store_keys<1>(lds[0], e);
-      if (quarter == 2) in.template store_values<0>(lds[0], lds_flags[0], e);
-      if (quarter == 3) in.template store_values<1>(lds[0], lds_flags[0], e);
-    }
-  if (tiles > 1) {
-    in.load_keys(begin + L::kTokens);
-    in.load_values(begin + L::kTokens);
-    in.pages(begin + 2 * L::kTokens, end);
-  }
+  for (int quarter = 0; quarter < 4; ++quarter) produce(quarter, -1, lds[0], lds_flags[0]);
   for (int i = 0; i < tiles; ++i) {
     const int t0 = begin + i * L::kTokens, b = i & 1;
     const char* const stage = lds[b];
     char* const next = lds[b ^ 1];
     uint8_t* const next_flags = lds_flags[b ^ 1];
-    const bool follows = i + 1 < tiles;
     __syncthreads();
-    const uint32_t flag = lane < L::kQuads / 2 ? reinterpret_cast<const uint32_t*>(lds_flags[b])[lane] : 0;
+    const uint32_t flag = lane < L::kFlags / 4 ? reinterpret_cast<const uint32_t*>(lds_flags[b])[lane] : 0;
     const bool odd = __any(flag != 0);  // pages or values that are not there
     if (PIPED && t0 >= all_lo && t0 + L::kTokens <= all_hi && !odd) {
+      // A step's products one after the other (the next step's scores, then this step's values), each beside a share of what
+      // the vector units have to do meanwhile (this step's numerators, then the next tile's way into LDS and the next
+      // step's maximum); their operands come from LDS kAhead products before. The order is kept by barriers.
+      constexpr int kAhead = 4, PS = 2 * CT, kAll = (ST - 1) * (KS + PS) + PS;
+      h8 ring[kAhead];
+      const auto fetch = [&](int n) {  // operand n of the tile
+        if (n >= kAll) return;
+        const int st = n / (KS + PS), j = n % (KS + PS) + (st == ST - 1 ? KS : 0);
+        ring[n % kAhead] = j < KS ? key(stage, st + 1, j) : value(stage, st, j - KS);
+      };
       f32x16 s = scores(stage, 0);
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) fetch(n);
+      refer(largest(s));
       h8 p[2];
 #pragma unroll
       for (int st = 0; st < ST; ++st) {
-        if (st > 0) weigh(stage, st - 1, p);
-        if (follows) {
-#pragma unroll
-          for (int k = 4 * st / ST; k < 4 * (st + 1) / ST; ++k) produce(k, i, next, next_flags);
-        }
-        refer(s);
+        const bool more = st + 1 < ST;
+        const int n0 = st * (KS + PS);
         f32x16 s_next;
-        if (st + 1 < ST) s_next = scores(stage, st + 1);
-        numerators(s, p);
-        if (st + 1 < ST) s = s_next;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s_next[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          if (more) {
+            s_next = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[(n0 + k) % kAhead], q[k], s_next, 0, 0, 0);
+            fetch(n0 + k + kAhead);
+          }
+#pragma unroll
+          for (int j = 16 * k / KS; j < 16 * (k + 1) / KS; j += 2) numerators(s, j, p);
+          if (more) __builtin_amdgcn_sched_barrier(0);
+        }
+        float most = -__builtin_inff();
+#pragma unroll
+        for (int j = 0; j < PS; ++j) {
+          const int n = n0 + (more ? KS : 0) + j;
+          o[j % CT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[n % kAhead], p[j / CT], o[j % CT], 0, 0, 0);
+          fetch(n + kAhead);
+          if (j == 0) {
+#pragma unroll
+            for (int k = 4 * st / ST; k < 4 * (st + 1) / ST; ++k) produce(k, i, next, next_flags);
+          }
+          if (more && j >= PS / 2) {
+#pragma unroll
+            for (int k = 32 * j / PS - 16; k < 32 * (j + 1) / PS - 16; ++k) most = fmaxf(most, s_next[k]);
+          }
+          if (j >= PS / 2) __builtin_amdgcn_sched_barrier(0);
+        }
+        if (more) {
+          s = s_next;
+          refer(most);
+        }
       }
-      weigh(stage, ST - 1, p);
       continue;
     }
     // ---- tiles that some of the wave's rows see in part
-    if (follows) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) produce(k, i, next, next_flags);
-    }
+    for (int k = 0; k < 4; ++k) produce(k, i, next, next_flags);
 #pragma unroll 1
     for (int st = 0; st < ST; ++st) {
       const int t1 = t0 + 32 * st;
@@ -384,18 +399,20 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int at = t1 + 4 * half + 8 * (j / 4) + j % 4;
-          const uint8_t* flags = &lds_flags[b][2 * (8 * st + 4 * (j / 8) + 2 * half + j / 4 % 2)];
+          const uint8_t* flags = &lds_flags[b][8 * st + 4 * (j / 8) + 2 * half + j / 4 % 2];
           const bool seen = at >= lo && at < hi && !(flags[0] & 16);
           if (!seen) s[j] = -__builtin_inff();
 #pragma unroll
           for (int c = 0; c < (HD + 127) / 128; ++c)
-            if (seen && (flags[c] >> (j % 4) & 1)) poisoned |= 1u << c;
+            if (seen && (flags[c * L::kQuads] >> (j % 4) & 1)) poisoned |= 1u << c;
         }
       }
-      refer(s);
+      refer(largest(s));
       h8 p[2];
-      numerators(s, p);
-      weigh(stage, st, p);
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) numerators(s, j, p);
+#pragma unroll
+      for (int j = 0; j < 2 * CT; ++j) o[j % CT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(value(stage, st, j), p[j / CT], o[j % CT], 0, 0, 0);
     }
   }
 
