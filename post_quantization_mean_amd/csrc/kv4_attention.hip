@@ -492,8 +492,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
 
 template <int HD, int NR, bool BF16>
 void launch_rows(const AttnArgs& a, hipStream_t stream) {
-  if (a.n_blocks) rows_kernel<HD, NR, BF16, true><<<dim3((unsigned)a.n_blocks), kWaves * 64, 0, stream>>>(a);
-  else rows_kernel<HD, NR, BF16, false><<<dim3((unsigned)a.n_tiles, (unsigned)a.c.n_kv), kWaves * 64, 0, stream>>>(a);
+  if (a.n_blocks) rows_kernel<HD, NR, BF16, true><<<attention_grid(a), kWaves * 64, 0, stream>>>(a);
+  else rows_kernel<HD, NR, BF16, false><<<attention_grid(a), kWaves * 64, 0, stream>>>(a);
 }
 
 template <bool BF16>
@@ -523,7 +523,8 @@ hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Rows of a sequence and key head up to which a block of the kernel above takes 32 of them; past that the kernel for prompts.
+// Rows of a sequence and key head up to which a block of the kernel above takes 32 of them; past that the kernel for prompts
+// (32 sequences of 32 rows over 6000 tokens: 75 us, as prompts 162; 16 of 128 rows over 9000: 157 us either way).
 constexpr int kFewRows = 64;
 
 size_t plan_attention(AttnArgs* a, bool ragged) {
@@ -538,10 +539,13 @@ size_t plan_attention(AttnArgs* a, bool ragged) {
   int64_t span = a->max_kv;
   if (a->window && a->causal) span = min(span, (int64_t)a->window + a->tile_rows / a->group + kAlign);
   const int hd = a->c.head_dim <= 64 ? 64 : a->c.head_dim <= 128 ? 128 : 256;
-  const int64_t live = a->tile_rows > 32 ? 1 : live_waves(hd * a->tile_rows / 16);
-  const int64_t units = (int64_t)a->n_tiles * a->c.n_kv * ((span + kUnit - 1) / kUnit);
-  a->n_blocks = (int)min(256 * live, units / kLeastUnits);
-  if (a->n_tiles > kMostTiles || (int64_t)a->n_tiles * a->c.n_kv >= 4 * 256 * live || span <= kLeastUnits * kUnit) a->n_blocks = 0;
+  const int64_t pairs = (int64_t)a->n_tiles * a->c.n_kv, units = pairs * ((span + kUnit - 1) / kUnit);
+  // Blocks of a split: as many as run at once. It costs some microseconds in each block and a second launch: not for short
+  // spans, many tiles, or tiles of prompts that fill the compute units without it (9 prompts of up to 1500 tokens, 880 tiles
+  // and key heads: 133 us, split 291; 128 of 128 rows over 9000 tokens: 218 us, split 160).
+  const int64_t at_once = 256 * (a->tile_rows > 32 ? 1 : live_waves(hd * a->tile_rows / 16));
+  a->n_blocks = (int)min(at_once, units / kLeastUnits);
+  if (a->n_tiles > kMostTiles || pairs >= at_once * (a->tile_rows > 32 ? 1 : 4) || span <= kLeastUnits * kUnit) a->n_blocks = 0;
   if (a->n_blocks == 0) return 0;
   return prefix_bytes(a->n_tiles) + (size_t)2 * a->n_blocks * a->tile_rows * (a->c.head_dim + 2) * sizeof(float);
 }

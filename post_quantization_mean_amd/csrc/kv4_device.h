@@ -137,13 +137,23 @@ __device__ __forceinline__ void unit_prefix(const AttnArgs& a, int* lds, RowTile
   __syncthreads();
 }
 
+// Blocks (key head, tile % kGridTiles, tile / kGridTiles), or a row of them that share the work.
+constexpr int kGridTiles = 32768;
+inline dim3 attention_grid(const AttnArgs& a) {
+  if (a.n_blocks) return dim3((unsigned)a.n_blocks);
+  return dim3((unsigned)a.c.n_kv, (unsigned)(a.n_tiles < kGridTiles ? a.n_tiles : kGridTiles), (unsigned)((a.n_tiles - 1) / kGridTiles + 1));
+}
+
 // Calls take(tile, key head, begin, end, part) for each piece of this block's work; part -1: a tile's whole span.
 template <bool SPLIT, typename F>
 __device__ __forceinline__ void for_pieces(const AttnArgs& a, int* lds, F take) {
   if constexpr (!SPLIT) {
-    const RowTile t = row_tile(a, a.n_tiles - 1 - (int)blockIdx.x);  // the last tiles of causal rows see the most
+    const int tile = (int)(blockIdx.z * kGridTiles + blockIdx.y);
+    if (tile >= a.n_tiles) return;
+    // the last tiles of causal rows see the most: all key heads' go first
+    const RowTile t = row_tile(a, a.n_tiles - 1 - tile);
     const KvSpan s = kv_span(a, t);
-    if (s.units) take(t, (int)blockIdx.y, s.begin, s.end, -1);
+    if (s.units) take(t, (int)blockIdx.x, s.begin, s.end, -1);
   } else {
     struct Piece {
       RowTile t;

@@ -464,7 +464,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
 template <int HD, int WAVES>
 void launch(const AttnArgs& a, bool bf16, hipStream_t stream) {
   static_assert(prompt_rows(HD) == 32 * WAVES, "rows of a block");
-  const dim3 grid = a.n_blocks ? dim3((unsigned)a.n_blocks) : dim3((unsigned)a.n_tiles, (unsigned)a.c.n_kv);
+  const dim3 grid = attention_grid(a);
   if (a.n_blocks) {
     if (bf16) prompt_kernel<HD, WAVES, true, true><<<grid, WAVES * 64, 0, stream>>>(a);
     else prompt_kernel<HD, WAVES, false, true><<<grid, WAVES * 64, 0, stream>>>(a);
