@@ -18,6 +18,20 @@ struct CHeads {
   int64_t ld, ld_head;
 };
 
+// Division of 0 <= n < 2^31 by a number known on the host: one multiplication (the quotient of n and the divisor is that of
+// n * (2^32 + mul) and 2^(32 + shift)).
+struct Divisor {
+  uint32_t mul, shift;
+  Divisor(uint32_t d = 1) {
+    shift = 0;
+    while (((uint64_t)1 << shift) < d) ++shift;
+    mul = (uint32_t)((((((uint64_t)1 << shift) - d) << 32) / d) + 1);
+  }
+#ifdef __HIPCC__
+  __device__ __forceinline__ int of(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+#endif
+};
+
 struct RopeArgs {
   CHeads x;
   Heads out;
@@ -31,6 +45,7 @@ struct RopeArgs {
   const int32_t* axis;
   float cos_scale, sin_scale;  // sin_scale = -cos_scale: the gradient
   bool in_place;
+  Divisor by_heads;  // by n_heads
 };
 hipError_t launch_rope(const RopeArgs& a, int dtype, bool pairs, hipStream_t stream);
 
@@ -51,20 +66,6 @@ struct Kv4MoveArgs {
 };
 hipError_t launch_kv4_write(const Kv4MoveArgs& a, int dtype, CHeads k, CHeads v, hipStream_t stream);
 hipError_t launch_kv4_read(const Kv4MoveArgs& a, int dtype, Heads k, Heads v, hipStream_t stream);
-
-// Division of 0 <= n < 2^31 by a number known on the host: one multiplication (the quotient of n and the divisor is that of
-// n * (2^32 + mul) and 2^(32 + shift)).
-struct Divisor {
-  uint32_t mul, shift;
-  Divisor(uint32_t d = 1) {
-    shift = 0;
-    while (((uint64_t)1 << shift) < d) ++shift;
-    mul = (uint32_t)((((((uint64_t)1 << shift) - d) << 32) / d) + 1);
-  }
-#ifdef __HIPCC__
-  __device__ __forceinline__ int of(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
-#endif
-};
 
 constexpr int kUnit = 128;  // cached tokens that the split counts in
 

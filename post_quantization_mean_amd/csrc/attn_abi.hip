@@ -104,7 +104,7 @@ int rope(const char* x_name, const void* x, int64_t ld_x, int64_t ld_x_head, int
   TRY(check_in_place(out_name, out, ld_out, ld_out_head, x_name, x, ld_x, ld_x_head, n_tokens, n_heads));
   const awq::RopeArgs a{{x, ld_x, ld_x_head}, {out, ld_out, ld_out_head}, n_tokens, (int)n_heads, (int)head_dim, (int)rot_dim,
                         positions, ld_positions, position_bytes == 8, n_axes, inv_freq, axis, scale,
-                        backward ? -scale : scale, out == x};
+                        backward ? -scale : scale, out == x, awq::Divisor((uint32_t)n_heads)};
   hipError_t e = awq::launch_rope(a, dtype, style == AWQ_ROPE_PAIRS, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, backward ? "rope_backward launch" : "rope launch");
   return ok();

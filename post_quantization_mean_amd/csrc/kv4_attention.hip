@@ -139,7 +139,7 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile
 size_t prefix_bytes(int n_tiles) { return ((size_t)(n_tiles + 1) * sizeof(int) + 255) / 256 * 256; }
 
 constexpr int live_waves(int hd_nr) { return hd_nr <= 64 ? 3 : hd_nr <= 256 ? 2 : 1; }
-constexpr int depth(int hd_nr) { return hd_nr <= 128 ? 3 : 2; }
+constexpr int depth(int hd_nr) { return hd_nr == 128 ? 3 : 2; }
 
 template <int HD, int NR, bool BF16, bool SPLIT>
 __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(AttnArgs a) {

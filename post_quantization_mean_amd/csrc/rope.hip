@@ -1,8 +1,9 @@
 // Rotary positions over one or several axes, and their gradient (the same rotation, backwards).
 //
-// Bound by memory: every element is read once and written once, with three operations on it. A thread holds the cosines
-// and sines of kVec pairs of one token and turns those pairs in head after head, so that an angle (float64: the product, its
-// reduction to a quarter turn; float32: the series) is formed once for many heads.
+// Bound by memory: every element is read once and written once, with three operations on it. An angle costs some forty
+// operations (float64: the product, its reduction to a quarter turn; float32: the series) and serves all heads of a token:
+// a block's threads form the cosines and sines of its tokens once, into LDS, and then turn the heads' pairs, kVec
+// a thread, with the loads of kRows heads on their way.
 #include "attn.h"
 #include "moe_device.h"
 
@@ -10,6 +11,7 @@ namespace awq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kStreamBytes = (int64_t)32 << 20;
 
 // cos and sin of position * freq. The quarter turns are taken off in float64 (pi / 2 in two parts), so that far positions lose
 // nothing; what is left, at most pi / 4, goes through the Taylor series in float32: the first terms left out are
@@ -36,68 +38,108 @@ __device__ __forceinline__ void cos_sin(int64_t position, float freq, float& c, 
   s = q & 2 ? -b : b;
 }
 
-// Block (x: token, y: part of the heads). Threads: items of a head (chunks of kVec pairs, then chunks of the channels that are
-// only copied) times heads.
-template <typename T, bool PAIRS>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int pair_items, int items, int heads_at_once) {
+// Tokens of a block: as many as its threads have angles.
+inline int tokens_of(int rot_dim) { return min(max(kThreads / (rot_dim / 2), 1), 16); }
+constexpr int kAngles = 256;  // of a block, at most: AWQ_MAX_ROPE_DIM / 2
+constexpr int kRows = 4;
+
+// Block (x: tokens, y: part of their rows; a row: one head of one token). Threads: items of a row (chunks of kVec pairs, then
+// chunks of the channels that are only copied) times rows.
+template <typename T, bool PAIRS, bool STREAM>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int tokens, int pair_items, int items, int rows_at_once) {
   constexpr int V = kVec<T>;
-  const int item = (int)threadIdx.x % items;
-  int head = (int)threadIdx.x / items + (int)blockIdx.y * heads_at_once;
-  if ((int)threadIdx.x >= items * heads_at_once) return;
-  const int64_t t = blockIdx.x;
-  const T* x = (const T*)a.x.p + t * a.x.ld + head * a.x.ld_head;
-  T* out = (T*)a.out.p + t * a.out.ld + head * a.out.ld_head;
-  const int step = heads_at_once * (int)gridDim.y;
-  const int64_t x_step = step * a.x.ld_head, out_step = step * a.out.ld_head;
+  __shared__ float2 turn[kAngles];
+  const int half = a.rot_dim / 2;
+  const int64_t first_token = (int64_t)blockIdx.x * tokens;
+  const int n = (int)min((int64_t)tokens, a.n_tokens - first_token);
+  for (int i = threadIdx.x; i < n * half; i += kThreads) {
+    const int t = i / half, pair = i - t * half;
+    const int axis = a.axis ? a.axis[pair] : 0;
+    int64_t p = 0;
+    if (axis >= 0 && axis < a.n_axes) {
+      const int64_t at = axis * a.ld_positions + first_token + t;
+      p = a.pos64 ? ((const int64_t*)a.positions)[at] : (int64_t)((const int32_t*)a.positions)[at];
+    }
+    float c, s;
+    cos_sin(p, a.inv_freq[pair], c, s);
+    turn[i] = make_float2(c * a.cos_scale, s * a.sin_scale);
+  }
+  __syncthreads();
+  const int item = (int)threadIdx.x % items, step = rows_at_once * (int)gridDim.y;
+  int row = (int)threadIdx.x / items + (int)blockIdx.y * rows_at_once;
+  if ((int)threadIdx.x >= items * rows_at_once) return;
+  const int rows = n * a.n_heads;
+  const T* const x = (const T*)a.x.p + first_token * a.x.ld;
+  T* const out = (T*)a.out.p + first_token * a.out.ld;
   if (item >= pair_items) {
     const int i = a.rot_dim + (item - pair_items) * V;
-    for (; head < a.n_heads; head += step, x += x_step, out += out_step) {
+    for (; row < rows; row += step) {
+      const int t = a.by_heads.of(row), head = row - t * a.n_heads;
       float v[V];
-      load_chunk(x, i, a.head_dim, v);
-      store_chunk(out, i, a.head_dim, v);
+      load_chunk(x + t * a.x.ld + head * a.x.ld_head, i, a.head_dim, v);
+      store_chunk(out + t * a.out.ld + head * a.out.ld_head, i, a.head_dim, v);
     }
     return;
   }
-  const int half = a.rot_dim / 2, first = item * V;
-  float c[V], s[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int i = min(first + k, half - 1);
-    const int axis = a.axis ? a.axis[i] : 0;
-    int64_t p = 0;
-    if (axis >= 0 && axis < a.n_axes)
-      p = a.pos64 ? ((const int64_t*)a.positions)[axis * a.ld_positions + t]
-                  : (int64_t)((const int32_t*)a.positions)[axis * a.ld_positions + t];
-    cos_sin(p, a.inv_freq[i], c[k], s[k]);
-    c[k] *= a.cos_scale;
-    s[k] *= a.sin_scale;
-  }
   // two chunks: the pairs' first and second channels, or the channels 2 first .. of adjacent pairs
+  const int first = item * V;
   const int at = PAIRS ? 2 * first : first, end = PAIRS ? a.rot_dim : half;
   const int at2 = PAIRS ? at + V : half + first, end2 = a.rot_dim;
-#pragma unroll 2
-  for (; head < a.n_heads; head += step, x += x_step, out += out_step) {
-    float u[V], w[V], p[V], q[V];
-    load_chunk(x, at, end, u);
-    load_chunk(x, at2, end2, w);
-    if constexpr (PAIRS) {
+  const bool whole = first + V <= half;  // both chunks
+  const auto place = [&](int r, int64_t ld, int64_t ld_head) {
+    const int t = a.by_heads.of(r);
+    return t * ld + (r - t * a.n_heads) * ld_head;
+  };
+  const auto rotate = [&](int r, const float (&u)[V], const float (&w)[V], float (&p)[V], float (&q)[V]) {
+    const float2* cs = turn + a.by_heads.of(r) * half;
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
+    for (int k = 0; k < V; ++k) {
+      const float2 z = cs[min(first + k, half - 1)];
+      if constexpr (PAIRS) {
         const float lo = 2 * k < V ? u[(2 * k) % V] : w[(2 * k) % V];
         const float hi = 2 * k < V ? u[(2 * k + 1) % V] : w[(2 * k + 1) % V];
-        const float lo2 = fmaf(lo, c[k], -(hi * s[k])), hi2 = fmaf(hi, c[k], lo * s[k]);
+        const float lo2 = fmaf(lo, z.x, -(hi * z.y)), hi2 = fmaf(hi, z.x, lo * z.y);
         if (2 * k < V) p[(2 * k) % V] = lo2, p[(2 * k + 1) % V] = hi2;
         else q[(2 * k) % V] = lo2, q[(2 * k + 1) % V] = hi2;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        p[k] = fmaf(u[k], c[k], -(w[k] * s[k]));
-        q[k] = fmaf(w[k], c[k], u[k] * s[k]);
+      } else {
+        p[k] = fmaf(u[k], z.x, -(w[k] * z.y));
+        q[k] = fmaf(w[k], z.x, u[k] * z.y);
       }
     }
-    store_chunk(out, at, end, p);
-    store_chunk(out, at2, end2, q);
+  };
+  if (whole) {
+    for (; row < rows; row += kRows * step) {
+      Chunk<T> raw[kRows][2];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {  // (past the last row: the first one again, not stored)
+        const T* from = x + place(row + k * step < rows ? row + k * step : row, a.x.ld, a.x.ld_head);
+        raw[k][0] = *reinterpret_cast<const Chunk<T>*>(from + at);
+        raw[k][1] = *reinterpret_cast<const Chunk<T>*>(from + at2);
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int r = row + k * step;
+        if (r >= rows) break;
+        float u[V], w[V], p[V], q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) u[j] = to_f32(raw[k][0].v[j]), w[j] = to_f32(raw[k][1].v[j]);
+        rotate(r, u, w, p, q);
+        T* to = out + place(r, a.out.ld, a.out.ld_head);
+        store_own<T, STREAM>(to, Place<T>(at, end + V), p);
+        store_own<T, STREAM>(to, Place<T>(at2, end2 + V), q);
+      }
+    }
+    return;
+  }
+  for (; row < rows; row += step) {
+    float u[V], w[V], p[V], q[V];
+    const T* from = x + place(row, a.x.ld, a.x.ld_head);
+    load_chunk(from, at, end, u);
+    load_chunk(from, at2, end2, w);
+    rotate(row, u, w, p, q);
+    T* to = out + place(row, a.out.ld, a.out.ld_head);
+    store_chunk(to, at, end, p);
+    store_chunk(to, at2, end2, q);
   }
 }
 
@@ -107,10 +149,19 @@ hipError_t launch(const RopeArgs& a, bool pairs, hipStream_t stream) {
   const int pair_items = (a.rot_dim / 2 + V - 1) / V;
   const int copies = a.in_place ? 0 : (a.head_dim - a.rot_dim + V - 1) / V;
   const int items = pair_items + copies;  // at most 128 (512 float32 channels that are copied)
-  const int at_once = min(kThreads / items, a.n_heads);
-  const dim3 grid((unsigned)a.n_tokens, 1);
-  if (pairs) rope_kernel<T, true><<<grid, kThreads, 0, stream>>>(a, pair_items, items, at_once);
-  else rope_kernel<T, false><<<grid, kThreads, 0, stream>>>(a, pair_items, items, at_once);
+  // few tokens: one a block, and its rows over several blocks, so that each thread has one or two
+  int tokens = tokens_of(a.rot_dim);
+  if (a.n_tokens < 256 * tokens) tokens = 1;
+  const int rows_at_once = kThreads / items;
+  const int rows = min((int64_t)tokens, a.n_tokens) * a.n_heads;
+  const int parts = a.n_tokens <= 64 ? min((rows + rows_at_once - 1) / rows_at_once, 64) : 1;
+  const dim3 grid((unsigned)((a.n_tokens + tokens - 1) / tokens), (unsigned)parts);
+  // an output that the second-level caches do not hold goes past them
+  const bool past = a.n_tokens * a.n_heads * a.rot_dim * (int64_t)sizeof(T) >= kStreamBytes;
+#define ROPE(P, S) rope_kernel<T, P, S><<<grid, kThreads, 0, stream>>>(a, tokens, pair_items, items, rows_at_once)
+  if (pairs) past ? ROPE(true, true) : ROPE(true, false);
+  else past ? ROPE(false, true) : ROPE(false, false);
+#undef ROPE
   return hipGetLastError();
 }
 
