@@ -10,8 +10,9 @@
 //   O^T = V^T P^T B holds the numerators of row m for tokens 4 g .. 4 g + 3 of two tiles of 16 tokens: what the first product
 //                 left in the lane. A holds the same tokens for channels m * HD/16 .. (4 bytes of each token for HD = 128);
 //                 two tokens' bytes beside each other are pairs of the contraction, channel by channel.
-// So no operand crosses a lane, and nothing goes through LDS until the waves join. Codes become float16 numbers offset +
-// code * step with one rounding (2^-11 of the number at most); 1.7 vector operations a code.
+// So no operand crosses a lane, and nothing goes through LDS until the waves join. Keys stay codes (0.6 vector operations each):
+// step and offset meet the scores, in float32. Values become float16 numbers offset + code * step with one rounding (2^-11
+// of the number at most; 1.7 operations a code).
 
 #include <type_traits>
 
@@ -28,7 +29,8 @@ template <int HD>
 struct Stage {
   static constexpr int KW = HD / 32;   // words of codes of a token in a lane (keys)
   static constexpr int VB = HD / 32;   // bytes of codes of a token in a lane (values)
-  uint32_t k[2][KW], kp[2];
+  static constexpr int G = (HD + 127) / 128;
+  uint32_t k[2][KW], kp[2][G];
   uint32_t v[8][(VB + 3) / 4], vp[8];
   bool there[2];
 };
@@ -41,7 +43,9 @@ struct Loader {
   const int32_t* table;
   int page_log2, page_mask, row_bytes, lane_pages, lane;
   uint32_t n_pages;
-  int k_at[(HD + 127) / 128], v_at, k_group, v_group;  // this lane's bytes of a row, its groups' params (in words)
+  int group_words;
+  // A lane's offsets, unsigned: added to an address that the wave shares, they need no registers of 64 bits.
+  uint32_t k_at[(HD + 127) / 128], kp_at, v_at, vp_at;  // bytes of codes, words of params
 
   // The pages of the wave's next 64 tiles of 16 tokens: lane i has tile i's (-1 past the end).
   __device__ __forceinline__ void pages(int t0, int stride, int end) {
@@ -49,7 +53,6 @@ struct Loader {
     lane_pages = t < end ? table[t >> page_log2] : -1;
   }
   __device__ __forceinline__ void load(Stage<HD>& s, int i, int t0) const {
-    const int g = lane >> 4, m = lane & 15;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int id = __builtin_amdgcn_readlane(lane_pages, 2 * i + h);
@@ -61,21 +64,22 @@ struct Loader {
       const uint8_t* vc = kc + v_codes;
       const uint32_t* vp = kp + v_params;
       if constexpr (HD == 64) {
-        const uint2 u = *reinterpret_cast<const uint2*>(kc + m * row_bytes + k_at[0]);
+        const uint2 u = *reinterpret_cast<const uint2*>(kc + k_at[0]);
         s.k[h][0] = u.x, s.k[h][1] = u.y;
       } else {
 #pragma unroll
         for (int c = 0; c < HD / 128; ++c) {
-          const uint4 u = *reinterpret_cast<const uint4*>(kc + m * row_bytes + k_at[c]);
+          const uint4 u = *reinterpret_cast<const uint4*>(kc + k_at[c]);
           s.k[h][4 * c] = u.x, s.k[h][4 * c + 1] = u.y, s.k[h][4 * c + 2] = u.z, s.k[h][4 * c + 3] = u.w;
         }
       }
-      s.kp[h] = kp[k_group + m];
-      const uint4 p = *reinterpret_cast<const uint4*>(vp + v_group + 4 * g);
+#pragma unroll
+      for (int c = 0; c < Stage<HD>::G; ++c) s.kp[h][c] = (kp + c * group_words)[kp_at];
+      const uint4 p = *reinterpret_cast<const uint4*>(vp + vp_at);
       s.vp[4 * h] = p.x, s.vp[4 * h + 1] = p.y, s.vp[4 * h + 2] = p.z, s.vp[4 * h + 3] = p.w;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint8_t* row = vc + (4 * g + j) * row_bytes + v_at;
+        const uint8_t* row = vc + j * row_bytes + v_at;
         if constexpr (HD == 64) s.v[4 * h + j][0] = *reinterpret_cast<const uint16_t*>(row);
         else if constexpr (HD == 128) s.v[4 * h + j][0] = *reinterpret_cast<const uint32_t*>(row);
         else {
@@ -87,7 +91,13 @@ struct Loader {
   }
 };
 
-// A lane's part of the queries: rows m of NR tiles, channels g * HD/4 .. . Zeros past the last row and channel.
+// First channel of step s of a lane's queries and keys: those of g HD/4 .. in turn, of heads past 128 first the first 128's.
+template <int HD>
+__device__ __forceinline__ int step_channel(int g, int s) {
+  return HD > 128 ? s / 4 * 128 + g * 32 + s % 4 * 8 : g * (HD / 4) + s * 8;
+}
+
+// A lane's part of the queries: rows m of NR tiles, channels step_channel .. . Zeros past the last row and channel.
 template <int HD, int NR, typename T>
 __device__ __forceinline__ void load_queries(const AttnArgs& a, const RowTile& t, int head, int lane, uint4 (&raw)[NR][HD / 32]) {
   const int g = lane >> 4, m = lane & 15;
@@ -98,16 +108,19 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const RowTile& t
     const T* row = (const T*)a.q.p + (int64_t)(t.token0 + token) * a.q.ld + (int64_t)(head * a.group + of) * a.q.ld_head;
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s) {
-      const int c = g * (HD / 4) + s * 8;
+      const int c = step_channel<HD>(g, s);
       raw[n][s] = __builtin_bit_cast(uint4, *reinterpret_cast<const Chunk<T>*>(row + (c < a.c.head_dim ? c : 0)));
     }
   }
 }
 
-// Their operand, in the order of token_codes, and what their scores are multiplied by (times log2(e)).
-template <int HD, int NR, bool BF16, typename T>
+// Their operand for raw_codes, and what their scores are multiplied by (times log2(e)): channels in the order 0, 4, 1, 5, 2, 6,
+// 3, 7, the odd ones over 16. sum: of a row's queries in each group; less: what the exponents of raw_codes add to their product,
+// with the sign turned, from which the product's accumulator starts.
+template <int HD, int NR, typename T>
 __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile& t, int lane, uint4 (&raw)[NR][HD / 32],
-                                                h8 (&q)[NR][HD / 32], float (&scale)[NR]) {
+                                                h8 (&q)[NR][HD / 32], float (&scale)[NR], float (&sum)[NR][Stage<HD>::G],
+                                                float (&less)[NR][Stage<HD>::G]) {
   const int g = lane >> 4, m = lane & 15;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
@@ -115,7 +128,7 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile
     float top = 0.f, nan = 0.f;
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s) {
-      if (!there || g * (HD / 4) + s * 8 >= a.c.head_dim) raw[n][s] = make_uint4(0, 0, 0, 0);
+      if (!there || step_channel<HD>(g, s) >= a.c.head_dim) raw[n][s] = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float x = raw_f32<T>(raw[n][s], k);
@@ -124,13 +137,29 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile
       }
     }
     float up, down;
-    query_range<BF16>(max_over_rows(top), a.scale, up, down);
+    query_range<true>(max_over_rows(top), a.scale, up, down);
     scale[n] = fmaxf(fabsf(a.scale) * down, 0x1p-126f) + sum_over_rows(nan);  // NaN for a row with a NaN or an infinity
+    float even[Stage<HD>::G] = {}, odd[Stage<HD>::G] = {};  // sums of what the operand holds
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s) {
+      // read again: the numbers of the first pass would not fit the registers
+      asm volatile("" : "+v"(raw[n][s].x), "+v"(raw[n][s].y), "+v"(raw[n][s].z), "+v"(raw[n][s].w));
       constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[n][s][k] = (_Float16)(raw_f32<T>(raw[n][s], order[k]) * up);
+      for (int k = 0; k < 8; ++k) {
+        const bool of16 = order[k] & 1;
+        const _Float16 x = (_Float16)(raw_f32<T>(raw[n][s], order[k]) * (of16 ? up * 0.0625f : up));
+        q[n][s][k] = x;
+        if (of16) odd[s / 4 % Stage<HD>::G] += (float)x;
+        else even[s / 4 % Stage<HD>::G] += (float)x;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < Stage<HD>::G; ++c) {
+      even[c] = sum_over_rows(even[c]);
+      odd[c] = sum_over_rows(odd[c]);
+      sum[n][c] = fmaf(16.f, odd[c], even[c]);
+      less[n][c] = -1024.f * (even[c] + odd[c]);
     }
   }
 }
@@ -145,7 +174,7 @@ template <int HD, int NR, bool BF16, bool SPLIT>
 __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(AttnArgs a) {
   constexpr int CT = HD / 16;  // channel tiles; a lane's channels are m * CT .. and, of the result, (4 g + i) * CT ..
   constexpr int kPitch = HD + 4;
-  __shared__ float lds_o[kWaves][16][kPitch];
+  __shared__ __align__(16) float lds_o[kWaves][16][kPitch];
   __shared__ float lds_m[kWaves][16 * NR], lds_l[kWaves][16 * NR];
   __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -178,12 +207,13 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
   // channels past the head's last one read others of the row: their queries are zeros, their results are not stored
 #pragma unroll
   for (int c = 0; c < (HD + 127) / 128; ++c) {
-    const int at = g * (HD / 8) + 16 * c;
-    in.k_at[c] = at < in.row_bytes ? at : 0;
+    const int at = g * (HD > 128 ? 16 : HD / 8) + (HD > 128 ? 64 : 16) * c;
+    in.k_at[c] = m * in.row_bytes + (at < in.row_bytes ? at : 0);
   }
-  in.k_group = min(g * (HD / 4) / 128, a.c.n_groups - 1) * page;
-  in.v_at = m * (HD / 32) < in.row_bytes ? m * (HD / 32) : 0;
-  in.v_group = min(m * CT / 128, a.c.n_groups - 1) * page;
+  in.group_words = page;
+  in.kp_at = m;
+  in.v_at = 4 * g * in.row_bytes + (m * (HD / 32) < in.row_bytes ? m * (HD / 32) : 0);
+  in.vp_at = min(m * CT / 128, a.c.n_groups - 1) * page + 4 * g;
 
   constexpr int kStride = kWaves * kStep;
   constexpr int D = depth(HD * NR);  // steps whose codes are in registers: the one in use and those on their way
@@ -196,9 +226,10 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       if (k == 0) in.pages(first, kStride, end);
       in.load(stage[k], k, first + k * kStride);
     }
+  constexpr int G = Stage<HD>::G;
   h8 q[NR][HD / 32];
-  float scale[NR];
-  convert_queries<HD, NR, BF16, T>(a, t, lane, raw, q, scale);
+  float scale[NR], q_sum[NR][G], q_less[NR][G];
+  convert_queries<HD, NR, T>(a, t, lane, raw, q, scale, q_sum, q_less);
 
   f32x4 o[NR][CT];
   float top[NR], sum[NR];  // the reference of a row's numerators, and their sum in this lane
@@ -212,22 +243,54 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
     for (int c = 0; c < CT; ++c) o[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
+  // The queries of heads past 128 wait in LDS, in the wave's own part of what the waves join in: the registers hold a second
+  // step's codes instead.
+  constexpr bool kAside = HD > 128;
+  static_assert(NR * HD * 2 <= kPitch * 4);
+  uint32_t aside = (uint32_t)lane;
+  if constexpr (kAside) {
+    h8* to = reinterpret_cast<h8*>(&lds_o[wave][0][0]);
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int i = 0; i < HD / 32; ++i) to[(n * (HD / 32) + i) * 64 + lane] = q[n][i];
+  }
+  const auto query = [&](int n, int i) {
+    if constexpr (kAside) return reinterpret_cast<const h8*>(&lds_o[wave][0][0])[(n * (HD / 32) + i) * 64 + aside];
+    else return q[n][i];
+  };
+
   const uint32_t e = code_exponent();
   // 32 tokens from t0 on
   const auto take = [&](Stage<HD>& now, int t0) {
-    // ---- scores
-    f32x4 s[NR][2];
+    // ---- scores: step * (q . codes) + offset * (sum of q), the products of codes without rounding
+    float x[NR][8];
+    if constexpr (kAside) asm volatile("" : "+v"(aside));  // read in every step
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t w = finite_or_nan(now.kp[h]);
-      const h2 p = as_h2(w), step = h2{p.x, p.x}, offset = h2{p.y, p.y};
 #pragma unroll
-      for (int n = 0; n < NR; ++n) s[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < G; ++c) {
+        f32x4 s[NR];
 #pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
-        const h8 k = token_codes(now.k[h][c], e, step, offset);
+        for (int n = 0; n < NR; ++n) s[n] = f32x4{q_less[n][c], q_less[n][c], q_less[n][c], q_less[n][c]};
 #pragma unroll
-        for (int n = 0; n < NR; ++n) s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][c], s[n][h], 0, 0, 0);
+        for (int i = 4 * c; i < min(4 * c + 4, HD / 32); ++i) {
+          const h8 k = raw_codes(now.k[h][i], e);
+#pragma unroll
+          for (int n = 0; n < NR; ++n) s[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, query(n, i), s[n], 0, 0, 0);
+        }
+        // lane m has token m's params; the scores are those of tokens 4 g .. 4 g + 3
+        const int w = (int)finite_or_nan(now.kp[h][c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const h2 p = as_h2((uint32_t)__builtin_amdgcn_ds_bpermute((4 * g + j) * 4, w));
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const float rest = c ? fmaf((float)p.y, q_sum[n][c], x[n][4 * h + j]) : (float)p.y * q_sum[n][c];
+            x[n][4 * h + j] = fmaf((float)p.x, s[n][j], rest);
+          }
+        }
+        if constexpr (HD > 128) __builtin_amdgcn_sched_barrier(0);
       }
     }
     const bool whole = t0 >= all_lo && t0 + kStep <= all_hi && t0 + kStep <= end && now.there[0] && now.there[1];
@@ -257,22 +320,18 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
     h8 p[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      float x[8], most = -__builtin_inff();
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[4 * h + j] = s[n][h][j];
+      float most = -__builtin_inff();
       if (rare(!whole)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int at = t0 + 16 * h + 4 * g + j;
-            if (at < lo[n] || at >= min(hi[n], end) || !now.there[h]) x[4 * h + j] = -__builtin_inff();
+            if (at < lo[n] || at >= min(hi[n], end) || !now.there[h]) x[n][4 * h + j] = -__builtin_inff();
           }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) most = fmaxf(most, x[j]);
+      for (int j = 0; j < 8; ++j) most = fmaxf(most, x[n][j]);
       most *= scale[n];
       // The numerators are powers from a reference that is set 2^7 below the largest score and moves only when they would
       // pass 2^15: float16 holds them, down to 2^-31 of the largest.
@@ -288,8 +347,8 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         // rounded towards zero, and summed as rounded: the weights add up to one, and the rounding's bias cancels
-        const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(fmaf(x[j], scale[n], -top[n])),
-                                                    __builtin_amdgcn_exp2f(fmaf(x[j + 1], scale[n], -top[n])));
+        const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(fmaf(x[n][j], scale[n], -top[n])),
+                                                    __builtin_amdgcn_exp2f(fmaf(x[n][j + 1], scale[n], -top[n])));
         const h2 pair = __builtin_bit_cast(h2, two);
         sum[n] = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum[n], false);
         p[n][j] = pair.x;

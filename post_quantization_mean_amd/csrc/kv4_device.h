@@ -250,11 +250,12 @@ __device__ __forceinline__ h8 token_codes(uint32_t w, uint32_t e, h2 step, h2 of
 
 // bfloat16 queries reach past float16: each row is brought to a largest magnitude in [1, 2) by a power of two (`up`), which the
 // scale of its scores takes back (`down`). What then lies below float16's normal numbers is below 2^-14 of the row's
-// largest. Negative scales are moved into the queries, so that the largest product is the largest score.
-template <bool BF16>
+// largest. Negative scales are moved into the queries, so that the largest product is the largest score. (FIT: as for
+// bfloat16.)
+template <bool FIT>
 __device__ __forceinline__ void query_range(float largest, float scale, float& up, float& down) {
   up = down = 1.f;
-  if constexpr (BF16) {
+  if constexpr (FIT) {
     const int e = min(max((int)(__float_as_uint(largest) >> 23) - 127, -126), 126);
     up = __uint_as_float((uint32_t)(127 - e) << 23);
     down = __uint_as_float((uint32_t)(127 + e) << 23);
@@ -281,6 +282,14 @@ __device__ __forceinline__ int fresh_lane() {
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));
   return lane;
+}
+
+// The same eight channels as they stand under the exponent: 1024 + code (channels 0, 4, 2, 6), 1024 + 16 code (1, 5, 3, 7).
+__device__ __forceinline__ h8 raw_codes(uint32_t w, uint32_t e) {
+  const uint32_t v = w >> 8;
+  const h2 a = as_h2((w & 0x000F000Fu) | e), b = as_h2((w & 0x00F000F0u) | e);
+  const h2 c = as_h2((v & 0x000F000Fu) | e), d = as_h2((v & 0x00F000F0u) | e);
+  return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
 // max or sum over the four rows of 16 lanes, in every lane
