@@ -346,10 +346,9 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       }
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        // rounded towards zero, and summed as rounded: the weights add up to one, and the rounding's bias cancels
-        const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(fmaf(x[n][j], scale[n], -top[n])),
-                                                    __builtin_amdgcn_exp2f(fmaf(x[n][j + 1], scale[n], -top[n])));
-        const h2 pair = __builtin_bit_cast(h2, two);
+        // summed as rounded, so that the weights add up to one
+        const h2 pair = to_h2(__builtin_amdgcn_exp2f(fmaf(x[n][j], scale[n], -top[n])),
+                              __builtin_amdgcn_exp2f(fmaf(x[n][j + 1], scale[n], -top[n])));
         sum[n] = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum[n], false);
         p[n][j] = pair.x;
         p[n][j + 1] = pair.y;

@@ -284,6 +284,12 @@ __device__ __forceinline__ int fresh_lane() {
   return lane;
 }
 
+// Two float16 numbers, rounded to the nearest.
+__device__ __forceinline__ h2 to_h2(float x, float y) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_convertvector((f32x2{x, y}), h2);
+}
+
 // The same eight channels as they stand under the exponent: 1024 + code (channels 0, 4, 2, 6), 1024 + 16 code (1, 5, 3, 7).
 __device__ __forceinline__ h8 raw_codes(uint32_t w, uint32_t e) {
   const uint32_t v = w >> 8;

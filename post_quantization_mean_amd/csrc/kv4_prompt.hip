@@ -288,10 +288,8 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
   };
   // two of a lane's sixteen numerators
   const auto numerators = [&](const f32x16& s, int j, h8 (&p)[2]) {
-    // rounded towards zero, and summed as rounded: the weights add up to one, and the rounding's bias cancels
-    const auto two = __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_exp2f(fmaf(s[j], scale, -top)),
-                                                __builtin_amdgcn_exp2f(fmaf(s[j + 1], scale, -top)));
-    const h2 pair = __builtin_bit_cast(h2, two);
+    // summed as rounded, so that the weights add up to one
+    const h2 pair = to_h2(__builtin_amdgcn_exp2f(fmaf(s[j], scale, -top)), __builtin_amdgcn_exp2f(fmaf(s[j + 1], scale, -top)));
     sum = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum, false);
     p[j / 8][j % 8] = pair.x;
     p[j / 8][j % 8 + 1] = pair.y;
