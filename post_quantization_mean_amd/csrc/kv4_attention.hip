@@ -11,8 +11,14 @@
 //                 left in the lane. A holds the same tokens for channels m * HD/16 .. (4 bytes of each token for HD = 128);
 //                 two tokens' bytes beside each other are pairs of the contraction, channel by channel.
 // So no operand crosses a lane, and nothing goes through LDS until the waves join. Keys stay codes (0.6 vector operations each):
-// step and offset meet the scores, in float32. Values become float16 numbers offset + code * step with one rounding (2^-11
-// of the number at most; 1.7 operations a code).
+// step and offset meet the scores, in float32. (Turned into float16 numbers first, as the values are, a float16 draft over 2048
+// tokens of heads of 256 was off by 3.3e-4 of its outputs' magnitude instead of 2.6e-4, 2.1e-4 of it the outputs' own rounding,
+// and the batch below took 91 us.) Values become float16 numbers offset + code * step with one rounding (2^-11 of the number at
+// most; 1.7 operations a code); numerators are rounded once, to the nearest.
+//
+// 64 sequences of up to 8192 tokens (ragged), 64 heads on 8 of 128: 84 us (3.6 TB/s), about 10 of them the shares' beginnings and
+// ends and 5 the joining kernel; as tiles of whole sequences, the longest ones' blocks alone at the end, 148 us. One token over
+// 131071: 41 us (3.5 TB/s).
 
 #include <type_traits>
 
@@ -115,7 +121,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const RowTile& t
 }
 
 // Their operand for raw_codes, and what their scores are multiplied by (times log2(e)): channels in the order 0, 4, 1, 5, 2, 6,
-// 3, 7, the odd ones over 16. sum: of a row's queries in each group; less: what the exponents of raw_codes add to their product,
+// 3, 7, the even ones times 16. sum: of a row's queries in each group; less: what the exponents of raw_codes add to their product,
 // with the sign turned, from which the product's accumulator starts.
 template <int HD, int NR, typename T>
 __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile& t, int lane, uint4 (&raw)[NR][HD / 32],
@@ -138,7 +144,7 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile
     }
     float up, down;
     query_range<true>(max_over_rows(top), a.scale, up, down);
-    scale[n] = fmaxf(fabsf(a.scale) * down, 0x1p-126f) + sum_over_rows(nan);  // NaN for a row with a NaN or an infinity
+    scale[n] = fmaxf(fabsf(a.scale) * (down * 0.0625f), 0x1p-126f) + sum_over_rows(nan);  // NaN for a row with a NaN or an infinity
     float even[Stage<HD>::G] = {}, odd[Stage<HD>::G] = {};  // sums of what the operand holds
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s) {
@@ -148,7 +154,7 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const bool of16 = order[k] & 1;
-        const _Float16 x = (_Float16)(raw_f32<T>(raw[n][s], order[k]) * (of16 ? up * 0.0625f : up));
+        const _Float16 x = (_Float16)(raw_f32<T>(raw[n][s], order[k]) * up * (of16 ? 1.f : 16.f));
         q[n][s][k] = x;
         if (of16) odd[s / 4 % Stage<HD>::G] += (float)x;
         else even[s / 4 % Stage<HD>::G] += (float)x;
@@ -164,11 +170,9 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile
   }
 }
 
-// Waves of a SIMD: what the registers of a variant let live.
-size_t prefix_bytes(int n_tiles) { return ((size_t)(n_tiles + 1) * sizeof(int) + 255) / 256 * 256; }
-
+// Waves of a SIMD: what the registers of a variant let live. (Heads of 128 with three: the token over 131071 46 us instead of 41,
+// since the work is split over half as many blocks again.)
 constexpr int live_waves(int hd_nr) { return hd_nr <= 64 ? 3 : hd_nr <= 256 ? 2 : 1; }
-constexpr int depth(int hd_nr) { return hd_nr == 128 ? 3 : 2; }
 
 template <int HD, int NR, bool BF16, bool SPLIT>
 __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(AttnArgs a) {
@@ -216,7 +220,9 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
   in.vp_at = min(m * CT / 128, a.c.n_groups - 1) * page + 4 * g;
 
   constexpr int kStride = kWaves * kStep;
-  constexpr int D = depth(HD * NR);  // steps whose codes are in registers: the one in use and those on their way
+  // Steps whose codes are in registers: the one in use and those on their way. (Three: the cases above 92 and 43 us, 64
+  // sequences of 8000 tokens of heads of 64 97 instead of 86.)
+  constexpr int D = 2;
   const int first = begin + wave * kStep;
   const int steps = first < end ? (end - first + kStride - 1) / kStride : 0;
   Stage<HD> stage[D];
@@ -584,6 +590,8 @@ hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
 // Rows of a sequence and key head up to which a block of the kernel above takes 32 of them; past that the kernel for prompts
 // (32 sequences of 32 rows over 6000 tokens: 75 us, as prompts 162; 16 of 128 rows over 9000: 157 us either way).
 constexpr int kFewRows = 64;
+
+size_t prefix_bytes(int n_tiles) { return ((size_t)(n_tiles + 1) * sizeof(int) + 255) / 256 * 256; }
 
 size_t plan_attention(AttnArgs* a, bool ragged) {
   const int64_t rows_each = (a->n_tokens + a->n_seqs - 1) / a->n_seqs * a->group;

@@ -250,8 +250,8 @@ __device__ __forceinline__ h8 token_codes(uint32_t w, uint32_t e, h2 step, h2 of
 
 // bfloat16 queries reach past float16: each row is brought to a largest magnitude in [1, 2) by a power of two (`up`), which the
 // scale of its scores takes back (`down`). What then lies below float16's normal numbers is below 2^-14 of the row's
-// largest. Negative scales are moved into the queries, so that the largest product is the largest score. (FIT: as for
-// bfloat16.)
+// largest. Negative scales are moved into the queries, so that the largest product is the largest score. FIT:
+// for such queries, and where they are multiplied by 16.
 template <bool FIT>
 __device__ __forceinline__ void query_range(float largest, float scale, float& up, float& down) {
   up = down = 1.f;

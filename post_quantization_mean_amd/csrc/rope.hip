@@ -3,7 +3,8 @@
 // Bound by memory: every element is read once and written once, with three operations on it. An angle costs some forty
 // operations (float64: the product, its reduction to a quarter turn; float32: the series) and serves all heads of a token:
 // a block's threads form the cosines and sines of its tokens once, into LDS, and then turn the heads' pairs, kVec
-// a thread, with the loads of kRows heads on their way.
+// a thread, with the loads of kRows heads on their way. 16384 tokens of 72 heads of 128 bf16: 114 us (5.3 TB/s, a large copy's
+// rate; one head's load at a time with its own cosines 170). One token of 40 heads: 2.5 us.
 #include "attn.h"
 #include "moe_device.h"
 
