@@ -122,7 +122,8 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const RowTile& t
 
 // Their operand for raw_codes, and what their scores are multiplied by (times log2(e)): channels in the order 0, 4, 1, 5, 2, 6,
 // 3, 7, the even ones times 16. sum: of a row's queries in each group; less: what the exponents of raw_codes add to their product,
-// with the sign turned, from which the product's accumulator starts.
+// with the sign turned, from which the product's accumulator starts. A row with a NaN or an infinity has NaN for every score (as
+// inf - inf); its scale stays a number, so that where it sees nothing it is nothing.
 template <int HD, int NR, typename T>
 __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile& t, int lane, uint4 (&raw)[NR][HD / 32],
                                                 h8 (&q)[NR][HD / 32], float (&scale)[NR], float (&sum)[NR][Stage<HD>::G],
@@ -131,20 +132,16 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     const bool there = t.row0 + 16 * n + m < t.rows;
-    float top = 0.f, nan = 0.f;
+    float top = 0.f;
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s) {
       if (!there || step_channel<HD>(g, s) >= a.c.head_dim) raw[n][s] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float x = raw_f32<T>(raw[n][s], k);
-        top = fmaxf(top, fabsf(x));
-        nan = fmaf(x, 0.f, nan);
-      }
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(raw_f32<T>(raw[n][s], k)));
     }
     float up, down;
     query_range<true>(max_over_rows(top), a.scale, up, down);
-    scale[n] = fmaxf(fabsf(a.scale) * (down * 0.0625f), 0x1p-126f) + sum_over_rows(nan);  // NaN for a row with a NaN or an infinity
+    scale[n] = fmaxf(fabsf(a.scale) * (down * 0.0625f), 0x1p-126f);
     float even[Stage<HD>::G] = {}, odd[Stage<HD>::G] = {};  // sums of what the operand holds
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s) {

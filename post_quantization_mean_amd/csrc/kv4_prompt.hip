@@ -234,12 +234,14 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
     }
     float up, down;
     query_range<BF16>(max_over_halves(size), a.scale, up, down);
-    scale = fmaxf(fabsf(a.scale) * down, 0x1p-126f) + sum_over_halves(nan);  // NaN for a row with a NaN or an infinity
+    scale = fmaxf(fabsf(a.scale) * down, 0x1p-126f);
+    // a row with a NaN or an infinity has NaN for every score, its scale stays a number: where it sees nothing it is nothing
+    nan = sum_over_halves(nan);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[s][k] = (_Float16)(raw_f32<T>(raw[s], order[k]) * up);
+      for (int k = 0; k < 8; ++k) q[s][k] = (_Float16)fmaf(raw_f32<T>(raw[s], order[k]), up, nan);
     }
   }
   // tokens that every row of the wave sees, and that any of them sees

@@ -109,6 +109,32 @@ def test_rows_that_see_nothing(attn):
     assert not bool(got.any())
 
 
+@pytest.mark.parametrize("q_len", [4, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_what_a_padding_query_holds_does_not_matter(attn, q_len, dtype):
+    """Queries of NaN and infinities: zeros where the row sees nothing (before the cache's beginning, or on pages outside it),
+    NaN where it sees a token, and no other row is touched."""
+    rng = np.random.default_rng(17)
+    codes, params = random_cache(rng, 40, 2, 64, 16)
+    c, p = cache_dev(codes, params)
+    table = torch.arange(40, dtype=torch.int32, device="cuda").reshape(2, 20)
+    table[1] = -1
+    kv_len = torch.tensor([q_len - 2, 60], dtype=torch.int32, device="cuda")  # the first sequence's rows 0, 1 see nothing
+    q = dev(rng.standard_normal((2 * q_len, 4, 64)), dtype)
+    clean, clean_lse = attn.awq_kv4_attention(q, c, p, table, kv_len, lse=True)
+    bad = q.clone()
+    bad[0, 0, 3], bad[1, 1, 5], bad[1, 2, :] = float("nan"), float("inf"), -float("inf")
+    bad[q_len:, :, 7] = float("nan")
+    bad[3, 1, 9], bad[3, 2, 8] = float("nan"), float("inf")
+    got, lse = attn.awq_kv4_attention(bad, c, p, table, kv_len, lse=True)
+    for x, y in ((got, clean), (lse, clean_lse)):
+        assert bool(x[3, 1:3].isnan().all())
+        x[3, 1:3] = y[3, 1:3]
+        assert torch.equal(x, y)
+    assert not bool(got[:2].any()) and not bool(got[q_len:].any())
+    assert bool((lse[:2] == -float("inf")).all()) and bool((lse[q_len:] == -float("inf")).all())
+
+
 def test_pages_outside_the_cache_are_not_seen(attn):
     rng = np.random.default_rng(5)
 
