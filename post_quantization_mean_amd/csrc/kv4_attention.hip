@@ -14,7 +14,7 @@
 // step and offset meet the scores, in float32. (Turned into float16 numbers first, as the values are, a float16 draft over 2048
 // tokens of heads of 256 was off by 3.3e-4 of its outputs' magnitude instead of 2.6e-4, 2.1e-4 of it the outputs' own rounding,
 // and the batch below took 91 us.) Values become float16 numbers offset + code * step with one rounding (2^-11 of the number at
-// most; 1.7 operations a code); numerators are rounded once, to the nearest.
+// most; 1.7 operations a code); numerators are rounded to the nearest.
 //
 // 64 sequences of up to 8192 tokens (ragged), 64 heads on 8 of 128: 84 us (3.6 TB/s), about 10 of them the shares' beginnings and
 // ends and 5 the joining kernel; as tiles of whole sequences, the longest ones' blocks alone at the end, 148 us. One token over
@@ -217,6 +217,11 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
   in.vp_at = min(m * CT / 128, a.c.n_groups - 1) * page + 4 * g;
 
   constexpr int kStride = kWaves * kStep;
+  // Float16 rows: a numerator is two float16 numbers, what the first one's rounding leaves is the second. The outputs' own rounding
+  // is no larger than the numerators' (a float16 draft over 2048 tokens of heads of 256: off by 2.6e-4 of its outputs' magnitude
+  // with one, 2.3e-4 with two, 2.1e-4 of it their own rounding). Bfloat16 rows have eight times that, and the second product would cost them 4 - 9 % (the
+  // batch above 90 us).
+  constexpr bool kRest = !BF16;
   // Steps whose codes are in registers: the one in use and those on their way. (Three: the cases above 92 and 43 us, 64
   // sequences of 8000 tokens of heads of 64 97 instead of 86.)
   constexpr int D = 2;
@@ -320,7 +325,7 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       }
     }
     // ---- numerators
-    h8 p[NR];
+    h8 p[NR], rest[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       float most = -__builtin_inff();
@@ -349,10 +354,17 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       }
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        // summed as rounded, so that the weights add up to one
-        const h2 pair = to_h2(__builtin_amdgcn_exp2f(fmaf(x[n][j], scale[n], -top[n])),
-                              __builtin_amdgcn_exp2f(fmaf(x[n][j + 1], scale[n], -top[n])));
-        sum[n] = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum[n], false);
+        const float x0 = __builtin_amdgcn_exp2f(fmaf(x[n][j], scale[n], -top[n]));
+        const float x1 = __builtin_amdgcn_exp2f(fmaf(x[n][j + 1], scale[n], -top[n]));
+        const h2 pair = to_h2(x0, x1);
+        if constexpr (kRest) {
+          const h2 less = to_h2(x0 - (float)pair.x, x1 - (float)pair.y);
+          rest[n][j] = less.x;
+          rest[n][j + 1] = less.y;
+          sum[n] += x0 + x1;
+        } else {  // summed as rounded, so that the weights add up to one
+          sum[n] = __builtin_amdgcn_fdot2(pair, h2{(_Float16)1.f, (_Float16)1.f}, sum[n], false);
+        }
         p[n][j] = pair.x;
         p[n][j + 1] = pair.y;
       }
@@ -379,7 +391,10 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       for (int c = 0; c < 4; ++c) {
         const h8 f = {v[c][0].x, v[c][0].y, v[c][1].x, v[c][1].y, v[c][2].x, v[c][2].y, v[c][3].x, v[c][3].y};
 #pragma unroll
-        for (int n = 0; n < NR; ++n) o[n][4 * b + c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[n], o[n][4 * b + c], 0, 0, 0);
+        for (int n = 0; n < NR; ++n) {
+          if constexpr (kRest) o[n][4 * b + c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, rest[n], o[n][4 * b + c], 0, 0, 0);
+          o[n][4 * b + c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[n], o[n][4 * b + c], 0, 0, 0);
+        }
       }
     }
   };

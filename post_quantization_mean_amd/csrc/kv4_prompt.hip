@@ -16,7 +16,7 @@
 // Rounding: keys and values become float16 numbers with one rounding each, 2^-11 of the number at most; numerators are rounded to
 // the nearest.
 //
-// 4096 tokens of 64 heads on 8 of 128 behind 8192: 1.47 - 1.50 ms (915 - 930 TFLOP/s; a large float16 library product reaches 1130
+// 4096 tokens of 64 heads on 8 of 128 behind 8192: 1.47 - 1.54 ms (890 - 930 TFLOP/s; a large float16 library product reaches 1130
 // on this card). 4096 causal tokens of 32 heads with their own keys: 175 us (785). 9 prompts of up to 1500 tokens, 32 heads on 8
 // of 64: 102 us; heads of 64 have half the products for each exponential (4 x 2048 tokens behind 2048: 300 us, 690 TFLOP/s;
 // as two blocks of four waves a compute unit 338, the prompts alike), heads of 256 one wave a SIMD (540).
