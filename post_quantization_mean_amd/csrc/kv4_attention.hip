@@ -122,8 +122,8 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const RowTile& t
 
 // Their operand for raw_codes, and what their scores are multiplied by (times log2(e)): channels in the order 0, 4, 1, 5, 2, 6,
 // 3, 7, the even ones times 16. sum: of a row's queries in each group; less: what the exponents of raw_codes add to their product,
-// with the sign turned, from which the product's accumulator starts. A row with a NaN or an infinity has NaN for every score (as
-// inf - inf); its scale stays a number, so that where it sees nothing it is nothing.
+// with the sign turned, from which the product's accumulator starts. A row with a NaN or an infinity has NaN for every score; its
+// scale stays a number, so that where it sees nothing it is nothing.
 template <int HD, int NR, typename T>
 __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile& t, int lane, uint4 (&raw)[NR][HD / 32],
                                                 h8 (&q)[NR][HD / 32], float (&scale)[NR], float (&sum)[NR][Stage<HD>::G],
@@ -140,7 +140,9 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile
       for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(raw_f32<T>(raw[n][s], k)));
     }
     float up, down;
-    query_range<true>(max_over_rows(top), a.scale, up, down);
+    top = max_over_rows(top);
+    query_range<true>(top, a.scale, up, down);
+    if (top == __builtin_inff()) up = __builtin_nanf("");  // (an infinity would be saturated)
     scale[n] = fmaxf(fabsf(a.scale) * (down * 0.0625f), 0x1p-126f);
     float even[Stage<HD>::G] = {}, odd[Stage<HD>::G] = {};  // sums of what the operand holds
 #pragma unroll
@@ -178,6 +180,7 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
   __shared__ __align__(16) float lds_o[kWaves][16][kPitch];
   __shared__ float lds_m[kWaves][16 * NR], lds_l[kWaves][16 * NR];
   __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
+  saturate_float16(true);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   for_pieces<SPLIT>(a, lds_prefix, [&](const RowTile& t, int head, int begin, int end, int part) {
   const int lane = fresh_lane(), g = lane >> 4, m = lane & 15;

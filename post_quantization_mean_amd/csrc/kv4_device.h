@@ -227,6 +227,15 @@ __device__ __forceinline__ uint32_t code_exponent() {
   return e;
 }
 
+// Memory that was never written may hold finite params whose numbers leave float16; as infinities such values would make NaNs of
+// the zeros that weigh what a row does not see. Hence values past float16's largest number count as it.
+// Sets the wave's mode in which float16 results do so by themselves. The matrix units take infinities and NaN among their float16
+// operands as numbers, too, then: a NaN has to come by float32.
+__device__ __forceinline__ void saturate_float16(bool on) {
+  constexpr int kMode = 1, kBit = 23;  // MODE.FP16_OVFL, one bit
+  __builtin_amdgcn_s_setreg(kMode | kBit << 6, on);
+}
+
 // Codes of bits 0 - 3 and 4 - 7 of both halves of u as offset + code * step, one rounding. A code under the exponent of
 // 1024 is 1024 + code (bits 0 - 3) or 1024 + 16 code (bits 4 - 7), from which the code itself comes back exactly.
 __device__ __forceinline__ h2 low_codes(uint32_t u, uint32_t e, h2 step, h2 offset) {

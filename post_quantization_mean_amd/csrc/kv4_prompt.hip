@@ -319,8 +319,10 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
     }
   };
 
+  saturate_float16(true);
 #pragma unroll
   for (int quarter = 0; quarter < 4; ++quarter) produce(quarter, -1, lds[0], lds_flags[0]);
+  saturate_float16(false);
   for (int i = 0; i < tiles; ++i) {
     const int t0 = begin + i * L::kTokens, b = i & 1;
     const char* const stage = lds[b];
@@ -332,7 +334,8 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
     if (PIPED && t0 >= all_lo && t0 + L::kTokens <= all_hi && !odd) {
       // A step's products one after the other (the next step's scores, then this step's values), each beside a share of what
       // the vector units have to do meanwhile (this step's numerators, then the next tile's way into LDS and the next
-      // step's maximum); their operands come from LDS kAhead products before. The order is kept by barriers.
+      // step's maximum); their operands come from LDS kAhead products before. The order is kept by barriers. The values'
+      // products may run with their conversion's mode: where a numerator is NaN, so is the row's sum.
       constexpr int kAhead = 4, PS = 2 * CT, kAll = (ST - 1) * (KS + PS) + PS;
       h8 ring[kAhead];
       const auto fetch = [&](int n) {  // operand n of the tile
@@ -363,6 +366,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
           if (more) __builtin_amdgcn_sched_barrier(0);
         }
         float most = -__builtin_inff();
+        saturate_float16(true);
 #pragma unroll
         for (int j = 0; j < PS; ++j) {
           const int n = n0 + (more ? KS : 0) + j;
@@ -378,6 +382,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
           }
           if (j >= PS / 2) __builtin_amdgcn_sched_barrier(0);
         }
+        saturate_float16(false);
         if (more) {
           s = s_next;
           refer(most);
@@ -386,8 +391,10 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
       continue;
     }
     // ---- tiles that some of the wave's rows see in part
+    saturate_float16(true);
 #pragma unroll
     for (int k = 0; k < 4; ++k) produce(k, i, next, next_flags);
+    saturate_float16(false);
 #pragma unroll 1
     for (int st = 0; st < ST; ++st) {
       const int t1 = t0 + 32 * st;
