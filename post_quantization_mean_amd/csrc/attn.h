@@ -92,8 +92,9 @@ struct AttnArgs {
   int n_blocks;    // 0: a block for each tile and key head; else blocks that share the cached tokens evenly (kv4_device.h)
   Divisor by_group, by_tiles, by_kv;  // by group, by the tiles of each sequence (where q_offsets is NULL), by n_kv
   int* prefix;     // with n_blocks: [n_tiles + 1] (the workspace's start)
-  float* part_o;   // [2 n_blocks][tile_rows][head_dim]
-  float* part_ml;  // [2 n_blocks][tile_rows][2]
+  float* part_o;     // [2 n_blocks][tile_rows][head_dim]
+  float* part_ml;    // [2 n_blocks][tile_rows][2]: reference (NaN: see part_base) and sum of the numerators
+  float* part_base;  // [2 n_blocks][tile_rows][2]: base and scale of the scores
 };
 
 // Fills the split from the sizes; returns the workspace's bytes.

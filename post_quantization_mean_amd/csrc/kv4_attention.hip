@@ -179,6 +179,7 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
   constexpr int kPitch = HD + 4;
   __shared__ __align__(16) float lds_o[kWaves][16][kPitch];
   __shared__ float lds_m[kWaves][16 * NR], lds_l[kWaves][16 * NR];
+  __shared__ float lds_base[kWaves][16 * NR], lds_scale[16 * NR];  // lds_scale: of rows with a base
   __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
   saturate_float16(true);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -244,11 +245,14 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
 
   f32x4 o[NR][CT];
   float top[NR], sum[NR];  // the reference of a row's numerators, and their sum in this lane
+  uint64_t based = 0;  // lanes whose reference has a base
   uint32_t poisoned[NR];  // groups (bits) whose values a row has seen a NaN in
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     top[n] = kNothing;
     sum[n] = 0.f;
+    lds_base[wave][16 * n + m] = 0.f;
+    lds_scale[16 * n + m] = scale[n];  // (the same of every wave)
     poisoned[n] = 0;
 #pragma unroll
     for (int c = 0; c < CT; ++c) o[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -343,17 +347,22 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmaxf(most, x[n][j]);
-      most *= scale[n];
       // The numerators are powers from a reference that is set 2^7 below the largest score and moves only when they would
       // pass 2^15: float16 holds them, down to 2^-31 of the largest.
-      if (rare(__any(most > top[n] + 15.f))) {
-        most = max_over_rows(most);
-        const float higher = fmaxf(most - 7.f, top[n]);
-        const float f = __builtin_amdgcn_exp2f(top[n] - higher);
-        top[n] = higher;
+      if (rare((based | __ballot(most * scale[n] > top[n] + kMost)) != 0)) {
+        float& base = lds_base[wave][16 * n + lane16_here()];
+        Reference ref = {top[n], base};
+        const float f = move_reference(ref, max_over_rows(most), scale[n]);
+        top[n] = ref.top;
         sum[n] *= f;
 #pragma unroll
         for (int c = 0; c < CT; ++c) o[n][c] *= f;
+        base = ref.base;
+        based |= __ballot(ref.base != 0.f);
+        if (based) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[n][j] -= ref.base;
+        }
       }
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -438,15 +447,29 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
     constexpr int kRowThreads = kWaves * 64 / 16;  // threads of a row
     const int row = (int)threadIdx.x / kRowThreads, r = t.row0 + 16 * n + row;
     if (r < t.rows) {
-      float most = kNothing;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) most = fmaxf(most, lds_m[w][16 * n + row]);
-      float f[kWaves], total = 0.f;
+      float most = kNothing, base = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        f[w] = __builtin_amdgcn_exp2f(lds_m[w][16 * n + row] - most);
-        total = fmaf(f[w], lds_l[w][16 * n + row], total);
+        most = fmaxf(most, lds_m[w][16 * n + row]);
+        base = fmaxf(base, fabsf(lds_base[w][16 * n + row]));
       }
+      float f[kWaves], total = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) f[w] = __builtin_amdgcn_exp2f(lds_m[w][16 * n + row] - most);
+      Reference ref = {most, 0.f};
+      float scale_of = 0.f;
+      if (rare(base != 0.f)) {
+        scale_of = lds_scale[16 * n + row];
+        const auto of_wave = [&](int w) { return Reference{lds_m[w][16 * n + row], lds_base[w][16 * n + row]}; };
+        ref = of_wave(0);
+#pragma unroll 1
+        for (int w = 1; w < kWaves; ++w)
+          if (between(of_wave(w), ref, scale_of) > 0.f) ref = of_wave(w);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) f[w] = __builtin_amdgcn_exp2f(between(of_wave(w), ref, scale_of));
+      }
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) total = fmaf(f[w], lds_l[w][16 * n + row], total);
       const int token = a.by_group.of(r), of = head * a.group + (r - token * a.group);
       const int64_t at = (int64_t)(t.token0 + token) * a.n_heads + of;
       const bool final = part < 0;
@@ -454,11 +477,11 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
       const float inv = final ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
       if ((int)threadIdx.x % kRowThreads == 0) {
         if (!final) {
-          float* ml = a.part_ml + 2 * slot;
-          ml[0] = most;
-          ml[1] = total;
+          const bool based = ref.base != 0.f;
+          reinterpret_cast<float2*>(a.part_ml)[slot] = make_float2(based ? __builtin_nanf("") : ref.top, total);
+          if (based) reinterpret_cast<float2*>(a.part_base)[slot] = make_float2(ref.base, scale_of);
         } else if (a.lse) {
-          a.lse[at] = total == 0.f ? -__builtin_inff() : (most + __log2f(total)) * kLn2;
+          a.lse[at] = log_of_sum(ref, scale_of, total);
         }
       }
       for (int c = (int)threadIdx.x % kRowThreads * 4; c < a.c.head_dim; c += kRowThreads * 4) {
@@ -516,17 +539,39 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
     }
   };
   load(mine);
-  float most = kNothing;
-  for (int i = lane; i < parts; i += 32) most = fmaxf(most, ((const float2*)a.part_ml)[part(i)].x);
+  float most = kNothing, nan = 0.f;
+  for (int i = lane; i < parts; i += 32) {
+    const float top = ((const float2*)a.part_ml)[part(i)].x;
+    most = fmaxf(most, top);
+    nan = fmaf(top, 0.f, nan);
+  }
 #pragma unroll
   for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
+  Reference ref = {most, 0.f};
+  float scale = 0.f;
+  const bool based = __any(nan != 0.f);
+  const auto of_part = [&](int i, float top) {
+    const bool here = __builtin_isnan(top);
+    const float2 b = here ? ((const float2*)a.part_base)[part(i)] : make_float2(0.f, 0.f);
+    if (here) scale = b.y;  // (of the row: the same in every part)
+    return reference(top, b.x);
+  };
+  if (rare(based)) {
+    for (int i = 0; i < parts; ++i) of_part(i, ((const float2*)a.part_ml)[part(i)].x);
+    ref = {kNothing, 0.f};
+    for (int i = 0; i < parts; ++i) {
+      const Reference of = of_part(i, ((const float2*)a.part_ml)[part(i)].x);
+      if (between(of, ref, scale) > 0.f) ref = of;
+    }
+  }
   float y[H][4] = {}, total = 0.f;
   for (int first = mine; first < parts; first += G * kJoin) {
     if (first != mine) load(first);
 #pragma unroll
     for (int k = 0; k < kJoin; ++k) {
       if (first + G * k >= parts) break;
-      const float f = __builtin_amdgcn_exp2f(w[k].x - most);
+      float f = __builtin_amdgcn_exp2f(w[k].x - most);
+      if (rare(based)) f = __builtin_amdgcn_exp2f(between(of_part(first + G * k, w[k].x), ref, scale));
       total = fmaf(f, w[k].y, total);
 #pragma unroll
       for (int h = 0; h < H; ++h)
@@ -557,7 +602,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
   if (!there) return;
   const int token = a.by_group.of(r), of = head * a.group + (r - token * a.group);
   if (lane == 0 && a.lse)
-    a.lse[(int64_t)(t.token0 + token) * a.n_heads + of] = total == 0.f ? -__builtin_inff() : (most + __log2f(total)) * kLn2;
+    a.lse[(int64_t)(t.token0 + token) * a.n_heads + of] = log_of_sum(ref, scale, total);
   const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
@@ -628,13 +673,15 @@ size_t plan_attention(AttnArgs* a, bool ragged) {
   a->n_blocks = (int)min(at_once, units / kLeastUnits);
   if (a->n_tiles > kMostTiles || pairs >= at_once * (a->tile_rows > 32 ? 1 : 4) || span <= kLeastUnits * kUnit) a->n_blocks = 0;
   if (a->n_blocks == 0) return 0;
-  return prefix_bytes(a->n_tiles) + (size_t)2 * a->n_blocks * a->tile_rows * (a->c.head_dim + 2) * sizeof(float);
+  return prefix_bytes(a->n_tiles) + (size_t)2 * a->n_blocks * a->tile_rows * (a->c.head_dim + 4) * sizeof(float);
 }
 
 void place_workspace(AttnArgs* a, void* workspace) {
   a->prefix = (int*)workspace;
   a->part_o = (float*)((char*)workspace + prefix_bytes(a->n_tiles));
-  a->part_ml = a->part_o + (size_t)2 * a->n_blocks * a->tile_rows * a->c.head_dim;
+  const size_t rows = (size_t)2 * a->n_blocks * a->tile_rows;
+  a->part_ml = a->part_o + rows * a->c.head_dim;
+  a->part_base = a->part_ml + 2 * rows;
 }
 
 hipError_t launch_kv4_attention(const AttnArgs& a, bool bf16, hipStream_t stream) {

@@ -286,6 +286,47 @@ __device__ __forceinline__ void store4(const AttnArgs& a, int64_t to, const floa
   }
 }
 
+// What a row's numerators are taken from: a score x (scale not yet applied) has the numerator 2^((x - base) * scale - top). base is 0,
+// and top lies kRoom below the largest score's exponent and moves when a numerator would pass 2^kMost, as long as top is below kWide.
+// Past it, where the reference's own rounding would count, base is the largest score and top -kRoom: exponents are
+// differences of scores then. Bases wait in LDS, and a wave that has one takes the branch that moves references in every step; the
+// others have a comparison more (drafts and heads of 256 2 % slower, single tokens and the long prompt alike).
+// Where a split's references are kept, NaN in the place of top says that there is a base.
+struct Reference {
+  float top, base;
+};
+constexpr float kRoom = 7.f, kMost = 15.f, kWide = 0x1p20f;
+__device__ __forceinline__ Reference reference(float top, float base) {
+  return __builtin_isnan(top) ? Reference{-kRoom, base} : Reference{top, 0.f};
+}
+
+// The base-2 exponent of numerators of reference a in those of reference b.
+__device__ __forceinline__ float between(const Reference& a, const Reference& b, float scale) {
+  return fmaf(a.base - b.base, scale, a.top - b.top);
+}
+
+// A row has met a score `most` (-infinity: none): moves its reference where it has to be, and gives the factor of the numerators so
+// far.
+__device__ __forceinline__ float move_reference(Reference& r, float most, float scale) {
+  const bool up = (most - r.base) * scale - kRoom > r.top, wide = fabsf(most * scale) > kWide;
+  const Reference to = {up ? (wide ? -kRoom : most * scale - kRoom) : r.top, up ? (wide ? most : 0.f) : r.base};
+  const float f = __builtin_amdgcn_exp2f(between(r, to, scale));
+  r = to;
+  return f;
+}
+
+// Lane % 16, worked out where it stands: kept from outside a branch, it would cost a register all along.
+__device__ __forceinline__ int lane16_here() {
+  int zero = 0;
+  asm volatile("" : "+v"(zero));
+  return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero)) % 16;
+}
+
+// log of a row's sum of exponentials
+__device__ __forceinline__ float log_of_sum(const Reference& r, float scale, float total) {
+  return total == 0.f ? -__builtin_inff() : fmaf(r.base, scale, r.top + __log2f(total)) * kLn2;
+}
+
 // The lane, which the compiler takes as new each time: what hangs on it is not kept in registers around a loop over pieces.
 __device__ __forceinline__ int fresh_lane() {
   int lane = threadIdx.x & 63;

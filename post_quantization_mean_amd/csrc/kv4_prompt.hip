@@ -192,6 +192,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
   __shared__ __attribute__((aligned(16))) char lds[2][L::kStage];
   __shared__ __attribute__((aligned(16))) uint8_t lds_flags[2][L::kFlags];
   __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
+  __shared__ float lds_base[WAVES * 32];  // of the rows' references
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   for_pieces<SPLIT>(a, lds_prefix, [&](const RowTile& t, int head, int begin, int end, int part) {
   const int lane = fresh_lane(), half = lane >> 5, m = lane & 31;
@@ -255,7 +256,9 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
   }
 
   f32x16 o[CT];
-  float top = kNothing, sum = 0.f;
+  float top = kNothing, sum = 0.f;  // the reference of the row's numerators, and their sum in this lane
+  uint64_t based = 0;  // lanes whose reference has a base
+  lds_base[wave * 32 + m] = 0.f;
   uint32_t poisoned = 0;  // groups (bits) whose values the row has seen a NaN in
 #pragma unroll
   for (int c = 0; c < CT; ++c)
@@ -276,16 +279,22 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
     return s;
   };
   // The numerators' reference: 2^7 below the largest score, moved only when a numerator would pass 2^15.
-  const auto refer = [&](float most) {
-    most *= scale;
-    if (rare(__any(most > top + 15.f))) {
-      most = max_over_halves(most);
-      const float higher = fmaxf(most - 7.f, top);
-      const float f = __builtin_amdgcn_exp2f(top - higher);
-      top = higher;
+  const auto refer = [&](f32x16& s, float most) {
+    if (rare((based | __ballot(most * scale > top + kMost)) != 0)) {
+      float& base = lds_base[wave * 32 + m];
+      Reference ref = {top, base};
+      const float f = move_reference(ref, max_over_halves(most), scale);
+      top = ref.top;
       sum *= f;
 #pragma unroll
       for (int c = 0; c < CT; ++c) o[c] *= f;
+      base = ref.base;
+      based = __ballot(ref.base != 0.f);
+    }
+    if (rare(based != 0)) {
+      const float base = lds_base[wave * 32 + m];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[j] -= base;
     }
   };
   const auto largest = [](const f32x16& s) {
@@ -346,7 +355,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
       f32x16 s = scores(stage, 0);
 #pragma unroll
       for (int n = 0; n < kAhead; ++n) fetch(n);
-      refer(largest(s));
+      refer(s, largest(s));
       h8 p[2];
 #pragma unroll
       for (int st = 0; st < ST; ++st) {
@@ -385,7 +394,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
         saturate_float16(false);
         if (more) {
           s = s_next;
-          refer(most);
+          refer(s, most);
         }
       }
       continue;
@@ -420,7 +429,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
             if (seen && (flags[c * L::kQuads] >> (j % 4) & 1)) poisoned |= 1u << c;
         }
       }
-      refer(largest(s));
+      refer(s, largest(s));
       h8 p[2];
 #pragma unroll
       for (int j = 0; j < 16; j += 2) numerators(s, j, p);
@@ -439,12 +448,12 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
     const int token = a.by_group.of(r), of = head * a.group + (r - token * a.group);
     const int64_t slot = (int64_t)part * a.tile_rows + (r - t.row0);
     if (half == 0) {
+      const float base = lds_base[wave * 32 + m];
       if (!final) {
-        float* ml = a.part_ml + 2 * slot;
-        ml[0] = top;
-        ml[1] = total;
+        reinterpret_cast<float2*>(a.part_ml)[slot] = make_float2(base != 0.f ? __builtin_nanf("") : top, total);
+        if (base != 0.f) reinterpret_cast<float2*>(a.part_base)[slot] = make_float2(base, scale);
       } else if (a.lse) {
-        a.lse[(int64_t)(t.token0 + token) * a.n_heads + of] = total == 0.f ? -__builtin_inff() : (top + __log2f(total)) * kLn2;
+        a.lse[(int64_t)(t.token0 + token) * a.n_heads + of] = log_of_sum({top, base}, scale, total);
       }
     }
     const float inv = final ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
