@@ -113,7 +113,7 @@ AWQ_API size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seq
  * tokens j < kv_len with j <= p (causal) and j > p - window (window > 0). For each head h (keys and values of head
  * h / (n_heads / n_kv)):
  *   out = sum over seen j of softmax_j(scale * q . k_j) v_j,  lse = log sum over seen j of exp(scale * q . k_j)
- * out = 0 and lse = -infinity where nothing is seen. Tokens on a page outside [0, n_pages) are not seen.
+ * out = 0 and lse = -infinity where nothing is seen (an lse past float32's range is an infinity, too). Tokens on a page outside [0, n_pages) are not seen.
  *   q          [n_tokens, n_heads, head_dim] of q_dtype (AWQ_DTYPE_BF16 or AWQ_DTYPE_F16).
  *   table      int32 [n_seqs, ld_table], table_width pages of each sequence used at most; kv_len is clamped to
  *              [0, table_width * page_size].

@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/awq_attn.h: argument checks, all before any HIP call, and the
 // launches. No allocation happens here; every buffer belongs to the caller.
+#include <float.h>
 #include <math.h>
 
 #include "abi_status.h"
@@ -306,7 +307,8 @@ int awq_kv4_attention(const void* q, int64_t ld_q, int64_t ld_q_head, int q_dtyp
   a.q_offsets = q_offsets;
   a.ld_table = ld_table;
   a.table_width = (int)table_width;
-  a.scale = scale * 1.44269504088896340736f;
+  const double in_base_2 = (double)scale * 1.44269504088896340736;  // float32's largest at most
+  a.scale = (float)fmin(fmax(in_base_2, -(double)FLT_MAX), (double)FLT_MAX);
   hipError_t e = awq::launch_kv4_attention(a, q_dtype == AWQ_DTYPE_BF16, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "kv4_attention launch");
   return ok();

@@ -143,7 +143,7 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const RowTile
     top = max_over_rows(top);
     query_range<true>(top, a.scale, up, down);
     if (top == __builtin_inff()) up = __builtin_nanf("");  // (an infinity would be saturated)
-    scale[n] = fmaxf(fabsf(a.scale) * (down * 0.0625f), 0x1p-126f);
+    scale[n] = fminf(fmaxf(fabsf(a.scale) * (down * 0.0625f), 0x1p-126f), kLargestFloat);
     float even[Stage<HD>::G] = {}, odd[Stage<HD>::G] = {};  // sums of what the operand holds
 #pragma unroll
     for (int s = 0; s < HD / 32; ++s) {
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
   constexpr int kPitch = HD + 4;
   __shared__ __align__(16) float lds_o[kWaves][16][kPitch];
   __shared__ float lds_m[kWaves][16 * NR], lds_l[kWaves][16 * NR];
-  __shared__ float lds_base[kWaves][16 * NR], lds_scale[16 * NR];  // lds_scale: of rows with a base
+  __shared__ float lds_base[kWaves][16 * NR], lds_scale[16 * NR];
   __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
   saturate_float16(true);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -253,6 +253,7 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
     sum[n] = 0.f;
     lds_base[wave][16 * n + m] = 0.f;
     lds_scale[16 * n + m] = scale[n];  // (the same of every wave)
+    scale[n] = scale_in_range(scale[n]);
     poisoned[n] = 0;
 #pragma unroll
     for (int c = 0; c < CT; ++c) o[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -457,16 +458,17 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) f[w] = __builtin_amdgcn_exp2f(lds_m[w][16 * n + row] - most);
       Reference ref = {most, 0.f};
-      float scale_of = 0.f;
+      float scale_of = 0.f;  // as it is
       if (rare(base != 0.f)) {
         scale_of = lds_scale[16 * n + row];
+        const float in_range = scale_in_range(scale_of);
         const auto of_wave = [&](int w) { return Reference{lds_m[w][16 * n + row], lds_base[w][16 * n + row]}; };
         ref = of_wave(0);
 #pragma unroll 1
         for (int w = 1; w < kWaves; ++w)
-          if (between(of_wave(w), ref, scale_of) > 0.f) ref = of_wave(w);
+          if (between(of_wave(w), ref, in_range) > 0.f) ref = of_wave(w);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) f[w] = __builtin_amdgcn_exp2f(between(of_wave(w), ref, scale_of));
+        for (int w = 0; w < kWaves; ++w) f[w] = __builtin_amdgcn_exp2f(between(of_wave(w), ref, in_range));
       }
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) total = fmaf(f[w], lds_l[w][16 * n + row], total);
@@ -561,7 +563,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
     ref = {kNothing, 0.f};
     for (int i = 0; i < parts; ++i) {
       const Reference of = of_part(i, ((const float2*)a.part_ml)[part(i)].x);
-      if (between(of, ref, scale) > 0.f) ref = of;
+      if (between(of, ref, scale_in_range(scale)) > 0.f) ref = of;
     }
   }
   float y[H][4] = {}, total = 0.f;
@@ -571,7 +573,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
     for (int k = 0; k < kJoin; ++k) {
       if (first + G * k >= parts) break;
       float f = __builtin_amdgcn_exp2f(w[k].x - most);
-      if (rare(based)) f = __builtin_amdgcn_exp2f(between(of_part(first + G * k, w[k].x), ref, scale));
+      if (rare(based)) f = __builtin_amdgcn_exp2f(between(of_part(first + G * k, w[k].x), ref, scale_in_range(scale)));
       total = fmaf(f, w[k].y, total);
 #pragma unroll
       for (int h = 0; h < H; ++h)

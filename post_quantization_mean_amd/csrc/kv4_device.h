@@ -10,7 +10,8 @@ namespace awq {
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
-constexpr float kNothing = -1e30f;  // the running maximum (of base-2 exponents) of a row that has seen nothing
+constexpr float kLargestFloat = 3.402823466e38f;
+constexpr float kNothing = -kLargestFloat;  // the reference of a row that has seen nothing
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kAlign = 32;  // cached tokens are taken in aligned runs of this many
 
@@ -300,6 +301,10 @@ __device__ __forceinline__ Reference reference(float top, float base) {
   return __builtin_isnan(top) ? Reference{-kRoom, base} : Reference{top, 0.f};
 }
 
+// A scale by which scores, below 2^41 and multiples of 2^-48 (of float16 numbers' products), stay above kNothing. Past it differences of scores
+// are 0 or decide alone, as they would anyway.
+__device__ __forceinline__ float scale_in_range(float scale) { return fminf(scale, 0x1p86f); }
+
 // The base-2 exponent of numerators of reference a in those of reference b.
 __device__ __forceinline__ float between(const Reference& a, const Reference& b, float scale) {
   return fmaf(a.base - b.base, scale, a.top - b.top);
@@ -322,7 +327,7 @@ __device__ __forceinline__ int lane16_here() {
   return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero)) % 16;
 }
 
-// log of a row's sum of exponentials
+// log of a row's sum of exponentials. scale: as it is, but finite
 __device__ __forceinline__ float log_of_sum(const Reference& r, float scale, float total) {
   return total == 0.f ? -__builtin_inff() : fmaf(r.base, scale, r.top + __log2f(total)) * kLn2;
 }

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
   __shared__ __attribute__((aligned(16))) char lds[2][L::kStage];
   __shared__ __attribute__((aligned(16))) uint8_t lds_flags[2][L::kFlags];
   __shared__ int lds_prefix[SPLIT ? kPrefixInts : 1];
-  __shared__ float lds_base[WAVES * 32];  // of the rows' references
+  __shared__ float lds_base[WAVES * 32], lds_scale[WAVES * 32];  // of the rows' references, and their scales as they are
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   for_pieces<SPLIT>(a, lds_prefix, [&](const RowTile& t, int head, int begin, int end, int part) {
   const int lane = fresh_lane(), half = lane >> 5, m = lane & 31;
@@ -235,7 +235,9 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
     }
     float up, down;
     query_range<BF16>(max_over_halves(size), a.scale, up, down);
-    scale = fmaxf(fabsf(a.scale) * down, 0x1p-126f);
+    const float as_is = fminf(fmaxf(fabsf(a.scale) * down, 0x1p-126f), kLargestFloat);
+    lds_scale[wave * 32 + m] = as_is;
+    scale = scale_in_range(as_is);
     // a row with a NaN or an infinity has NaN for every score, its scale stays a number: where it sees nothing it is nothing
     nan = sum_over_halves(nan);
 #pragma unroll
@@ -451,9 +453,9 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : 1) void prompt_kernel(
       const float base = lds_base[wave * 32 + m];
       if (!final) {
         reinterpret_cast<float2*>(a.part_ml)[slot] = make_float2(base != 0.f ? __builtin_nanf("") : top, total);
-        if (base != 0.f) reinterpret_cast<float2*>(a.part_base)[slot] = make_float2(base, scale);
+        if (base != 0.f) reinterpret_cast<float2*>(a.part_base)[slot] = make_float2(base, lds_scale[wave * 32 + m]);
       } else if (a.lse) {
-        a.lse[(int64_t)(t.token0 + token) * a.n_heads + of] = log_of_sum({top, base}, scale, total);
+        a.lse[(int64_t)(t.token0 + token) * a.n_heads + of] = log_of_sum({top, base}, lds_scale[wave * 32 + m], total);
       }
     }
     const float inv = final ? (total == 0.f ? 0.f : 1.f / total) : 1.f;

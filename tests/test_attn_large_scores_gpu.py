@@ -103,3 +103,41 @@ def test_scores_of_every_size_in_one_row(attn, q_len, kv_len, dtype):
         cache, table, v = _cache(rng, kv_len, d, codes[turn], 1.0, 0.0)
         for e in (4, 10, 13, 14, 20, 40):
             _check(attn, q, codes[turn].astype(np.float64), v, cache, table, np.log(2.0) * 2.0 ** e, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("q_len,kv_len", SHAPES)
+def test_scores_far_below_zero_are_seen(attn, q_len, kv_len, dtype):
+    """Scores from -2^30 down to below float32's range, by the queries' size and by the scale's: the largest of them has the weight. A
+    logarithm past float32 is -infinity, and the row has its weights all the same."""
+    rng = np.random.default_rng(q_len * kv_len)
+    d, heads = 64, 2
+    codes = np.zeros((kv_len, d), np.uint8)
+    codes[:, 5] = rng.integers(0, 16, kv_len)
+    cache, table, v = _cache(rng, kv_len, d, codes, 32.0, 32768.0)
+    k = 32768.0 + 32.0 * codes
+    lens = torch.tensor([kv_len], dtype=torch.int32, device="cuda")
+    print(f"[gpu large scores] below q={q_len} kv={kv_len} {dtype}", flush=True)
+    sizes = [(0, e) for e in (10, 70, 90, 100, 105, 120, 127)]
+    if dtype == "bf16":
+        sizes += [(e, 0) for e in (70, 90, 105, 120)] + [(100, 40), (126, 127), (-120, 127)]
+    for of_query, of_scale in sizes:
+        for sign in (-1.0, 1.0):
+            q = np.full((q_len, heads, d), sign * 2.0 ** of_query)
+            q[..., 5] *= 2.0 ** -7
+            got, lse = attn.awq_kv4_attention(dev(q, dtype), *cache, table, lens, scale=2.0 ** of_scale, max_kv=kv_len,
+                                              out_dtype=torch.float32, lse=True)
+            x = k @ (q[0, 0] / 2.0 ** of_query)  # exact, the same for every row
+            for i in range(q_len):
+                n = kv_len - q_len + i + 1
+                e = np.longdouble(2.0) ** (of_query + of_scale)
+                w = np.exp(np.maximum((x[:n] - x[:n].max()) * e, -11000)).astype(np.float64)
+                want = w @ v[:n] / w.sum()
+                # longdouble holds what float64 does not; float32's range ends at 2^128
+                log = float(x[:n].max() * e + np.log(np.longdouble(w.sum())))
+                tol = (w @ np.abs(v[:n]) / w.sum()) * (2.0 ** -10 + 2.0 ** -16 + n * 2.0 ** -24) + n * 2.0 ** -31 * 8
+                within(host(got[i]), np.broadcast_to(want, (heads, d)), np.broadcast_to(tol, (heads, d)), f"out {of_query} {of_scale} {sign}")
+                if abs(log) < 2.0 ** 127 * 1.99:
+                    within(host(lse[i]), np.full(heads, log), np.full(heads, abs(log) * 2.0 ** -21 + 2.0 ** -9), "lse")
+                elif abs(log) > 2.0 ** 128:
+                    assert bool((lse[i] == (float("inf") if log > 0 else -float("inf"))).all()), (of_query, of_scale, sign)
