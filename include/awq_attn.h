@@ -104,7 +104,7 @@ AWQ_API int awq_kv4_read(const uint8_t* codes, int64_t page_codes, const void* p
 
 /* ------------------------------------------------------------------ attention over the cache */
 
-/* Workspace bytes of awq_kv4_attention (0 on invalid sizes, and where none is needed). max_kv as there. */
+/* Workspace bytes of awq_kv4_attention (0 on invalid sizes, and where none is needed). max_kv as there; 0: enough for any table. */
 AWQ_API size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int ragged, int64_t n_heads,
                                                  int64_t n_kv, int64_t head_dim, int causal, int64_t window, int64_t max_kv);
 

@@ -254,8 +254,8 @@ size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int r
     ok();  // a query leaves no error behind
     return 0;
   }
-  size_t bytes;
-  attention_plan(n_tokens, n_seqs, ragged != 0, n_heads, n_kv, head_dim, causal, window, max_kv, &bytes);
+  size_t bytes;  // (of max_kv 0: enough for any table)
+  attention_plan(n_tokens, n_seqs, ragged != 0, n_heads, n_kv, head_dim, causal, window, max_kv ? max_kv : kMostKv, &bytes);
   return bytes;
 }
 
