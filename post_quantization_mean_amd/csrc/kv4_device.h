@@ -28,19 +28,18 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs& a, int tile) {
   RowTile r;
   int q_len, local;
   if (a.q_offsets) {
+    const auto offset = [&](int seq) { return min(max(a.q_offsets[seq], 0), (int)a.n_tokens); };
+    const auto first_tile = [&](int seq) { return (int)((int64_t)offset(seq) * a.group >> a.tile_log2) + seq; };
     int lo = 0, hi = a.n_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (((int64_t)a.q_offsets[mid] * a.group >> a.tile_log2) + mid <= tile) lo = mid;
+      if (first_tile(mid) <= tile) lo = mid;
       else hi = mid - 1;
     }
     r.seq = lo;
-    const int64_t begin = min(max((int64_t)a.q_offsets[lo], (int64_t)0), a.n_tokens);
-    const int64_t end = min(max((int64_t)a.q_offsets[lo + 1], begin), a.n_tokens);
-    r.token0 = (int)begin;
-    q_len = (int)(end - begin);
-    const int64_t first = ((int64_t)a.q_offsets[lo] * a.group >> a.tile_log2) + lo;
-    local = first <= tile && tile - first <= 0x7FFFFFFF >> a.tile_log2 ? (int)(tile - first) : -1;
+    r.token0 = offset(lo);
+    q_len = max(offset(lo + 1) - r.token0, 0);
+    local = tile - first_tile(lo);
   } else {
     const int tiles = (a.each * a.group + a.tile_rows - 1) >> a.tile_log2;
     r.seq = a.by_tiles.of(tile);
