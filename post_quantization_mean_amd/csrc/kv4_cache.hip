@@ -95,13 +95,25 @@ __device__ __forceinline__ void store8(T* row, int i, const float (&x)[8]) {
   }
 }
 
-// float16 bits of v >= 0, rounded once: to float32 towards zero with the lost bits' presence kept in the lowest one, then
-// to nearest even.
-__device__ __forceinline__ uint32_t f16_of(double v) {
+// float32 of v towards zero with the lost bits' presence kept in the lowest one: what rounds it to 16 bits rounds v.
+__device__ __forceinline__ float odd_f32(double v) {
   float f = (float)v;
-  if ((double)f > v) f = __uint_as_float(__float_as_uint(f) - 1);
+  if (fabs((double)f) > fabs(v)) f = __uint_as_float(__float_as_uint(f) - 1);
   if ((double)f != v) f = __uint_as_float(__float_as_uint(f) | 1);
-  return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f);
+  return f;
+}
+
+// float16 bits of v >= 0, rounded once.
+__device__ __forceinline__ uint32_t f16_of(double v) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)odd_f32(v));
+}
+
+// Is offset + c * step a float32 for every code c? A product has 15 bits, so it is where the exponents do not lie far apart: then the sum's
+// highest bit is at most 2^max(o, s + 4) * 2 and its lowest at least 2^(min(o, s) - 10). (The exponents: of float16, that of subnormal numbers
+// and zero as 1 is the one of their lowest bit's place. An offset of zero adds nothing.)
+__device__ __forceinline__ bool sums_are_exact(uint32_t params) {
+  const int s = max((int)(params >> 10 & 31), 1), o = max((int)(params >> 26 & 31), 1);
+  return (params & 0x7FFF0000u) == 0 || max(o, s + 4) - min(o, s) <= 12;
 }
 
 // float16 bits of (hi - lo) / 15, rounded once. float32's quotient is within 3 of its steps of the true one (the difference,
@@ -224,6 +236,11 @@ __global__ __launch_bounds__(kThreads) void read_kernel(Kv4MoveArgs a, Heads k, 
     float x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = fmaf((float)(word >> (4 * j) & 15u), step, offset);
+    // 16 bits: not by way of a rounded float32
+    if (sizeof(T) == 2 && __builtin_expect(!sums_are_exact(p), 0)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = odd_f32((double)(word >> (4 * j) & 15u) * (double)step + (double)offset);
+    }
     store8((T*)to.p + t * to.ld + head * to.ld_head, channel, x);
   }
 }
