@@ -81,7 +81,7 @@ AWQ_API int awq_rope_backward(const void* d_out, int64_t ld_d_out, int64_t ld_d_
 
 /* Quantizes the keys and values of n_tokens tokens into their slots. For each token, head and group, with x clamped to
  * +-AWQ_KV4_LARGEST:
- *   step   = float16((max x - min x) / 15), offset = float16(min x), each rounded once;
+ *   step   = float16((max x - min x) / 15), offset = float16(min x), each rounded once (the quotient as in float64);
  *   code   = min(max(round_to_even((x - offset) / step), 0), 15), the quotient before its rounding as in float64
  *            (0 where step is 0).
  * A group that holds a NaN or an infinity gets NaN for step and offset.
@@ -121,6 +121,8 @@ AWQ_API size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seq
  *   q_offsets  int32 [n_seqs + 1], ascending, or NULL: n_tokens / n_seqs new tokens for each (n_tokens is a multiple of
  *              n_seqs then). Rows of out and lse that belong to no sequence are left as they were.
  * n_tokens * n_heads is at most 2^27, table_width * page_size at most 2^30.
+ * One kernel, for few rows or for many, takes all sequences of a call; which one goes by the mean of n_tokens / n_seqs *
+ * n_heads / n_kv. A call that mixes single tokens and a long prompt is right, but two calls are faster.
  *   max_kv     the largest kv_len, as far as the caller knows: how the work is split goes by it, what is computed does not
  *              (up to the order of sums). 0: table_width * page_size.
  *   out        [n_tokens, n_heads, head_dim] of out_dtype (q_dtype or AWQ_DTYPE_F32). May be q, of the same type and pitches.

@@ -247,6 +247,7 @@ def awq_kv4_read(codes: torch.Tensor, params: torch.Tensor, slots: torch.Tensor,
 
 def awq_kv4_attention_workspace_bytes(n_tokens: int, n_seqs: int, ragged: bool, n_heads: int, n_kv: int, head_dim: int,
                                       causal: bool, window: int, max_kv: int) -> int:
+    """max_kv 0: enough for any table."""
     return _load().awq_kv4_attention_workspace_bytes(n_tokens, n_seqs, ragged, n_heads, n_kv, head_dim, causal, window, max_kv)
 
 
@@ -260,7 +261,8 @@ def awq_kv4_attention(q: torch.Tensor, codes: torch.Tensor, params: torch.Tensor
     usually the last of them, are kv_len[s] (int32) in the pages table[s] (int32 [n_seqs, width]). New token i stands at
     p = kv_len - q_len + i and sees cached tokens j <= p (causal) and j > p - window (window > 0). scale: head_dim ** -0.5
     unless given. max_kv: the largest kv_len, by which the work is split (0: what the table can hold). A token that sees
-    nothing gets zeros; rows that belong to no sequence are left as they were (zeros in a new tensor). `out` may be q.
+    nothing gets zeros; rows that belong to no sequence are left as they were (zeros in a new tensor). `out` may be q. One kernel takes
+    all sequences of a call: single tokens and long prompts are faster in calls of their own.
     lse: a float32 [n_tokens, n_heads] tensor that receives the logarithm of each row's sum, or True for a new one; then
     (out, lse) is returned."""
     if stream is not None:

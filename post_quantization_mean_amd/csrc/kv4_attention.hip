@@ -223,8 +223,9 @@ __global__ __launch_bounds__(kWaves * 64, live_waves(HD * NR)) void rows_kernel(
   constexpr int kStride = kWaves * kStep;
   // Float16 rows: a numerator is two float16 numbers, what the first one's rounding leaves is the second. The outputs' own rounding
   // is no larger than the numerators' (a float16 draft over 2048 tokens of heads of 256: off by 2.6e-4 of its outputs' magnitude
-  // with one, 2.3e-4 with two, 2.1e-4 of it their own rounding). Bfloat16 rows have eight times that, and the second product would cost them 4 - 9 % (the
-  // batch above 90 us).
+  // with one, 2.3e-4 with two, 2.1e-4 of it their own rounding). The second product costs 0 - 11 % (one token over 131071 40.5 ->
+  // 42.7 us, 32 drafts of 4 over 6000 76 -> 84). Bfloat16 rows do without it: in bfloat16 their outputs' own rounding is eight times as
+  // large; float32 outputs of bfloat16 queries have the numerators' 2^-11 each, an error of the size of the values' own rounding.
   constexpr bool kRest = !BF16;
   // Steps whose codes are in registers: the one in use and those on their way. (Three: the cases above 92 and 43 us, 64
   // sequences of 8000 tokens of heads of 64 97 instead of 86.)
@@ -650,7 +651,7 @@ hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Rows of a sequence and key head up to which a block of the kernel above takes 32 of them; past that the kernel for prompts
-// (32 sequences of 32 rows over 6000 tokens: 75 us, as prompts 162; 16 of 128 rows over 9000: 157 us either way).
+// (32 sequences of 32 rows over 6000 tokens: 76 us, as prompts 162; 16 of 128 rows over 9000: 157 us either way).
 constexpr int kFewRows = 64;
 
 size_t prefix_bytes(int n_tiles) { return ((size_t)(n_tiles + 1) * sizeof(int) + 255) / 256 * 256; }
@@ -669,8 +670,8 @@ size_t plan_attention(AttnArgs* a, bool ragged) {
   const int hd = a->c.head_dim <= 64 ? 64 : a->c.head_dim <= 128 ? 128 : 256;
   const int64_t pairs = (int64_t)a->n_tiles * a->c.n_kv, units = pairs * ((span + kUnit - 1) / kUnit);
   // Blocks of a split: as many as run at once. It costs some microseconds in each block and a second launch: not for short
-  // spans, many tiles, or tiles of prompts that fill the compute units without it (9 prompts of up to 1500 tokens, 880 tiles
-  // and key heads: 133 us, split 291; 128 of 128 rows over 9000 tokens: 218 us, split 160).
+  // spans, many tiles, or tiles of prompts that fill the compute units without it (9 prompts of up to 1500 tokens, 776 tiles
+  // and key heads: 133 us at the time, split 291; 128 of 128 rows over 9000 tokens: 218 us, split 160).
   const int64_t at_once = 256 * (a->tile_rows > 32 ? 1 : live_waves(hd * a->tile_rows / 16));
   a->n_blocks = (int)min(at_once, units / kLeastUnits);
   if (a->n_tiles > kMostTiles || pairs >= at_once * (a->tile_rows > 32 ? 1 : 4) || span <= kLeastUnits * kUnit) a->n_blocks = 0;

@@ -1,6 +1,7 @@
 // The paged cache of 4-bit keys and values: quantizing new tokens into their slots, and reading slots back.
 //
-// Both are bound by memory: a head's row of 128 16-bit channels is 256 bytes outside and 68 bytes in the cache. To write, a group
+// A head's row of 128 16-bit channels is 256 bytes outside and 68 bytes in the cache. Reading back is bound by memory; writing by the latency
+// of blocks that load, work and store once (neither memory nor the vector units are full). To write, a group
 // (up to 128 consecutive channels) belongs to kLanes = 2, 4 or 8 neighbouring lanes of 16 channels each, which find its minimum
 // and maximum by lane exchanges; to read, to 4, 8 or 16 lanes of 8 channels. A block takes a head of 16 to 256 consecutive
 // tokens, keys or values, so that the 64-byte rows of codes and the 4-byte parameters of tokens in consecutive slots are
@@ -143,7 +144,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float step, fl
   return lo | hi << 16;
 }
 
-// Bound by memory only while an element costs no more than some 15 vector operations: hence the decisions in float32, the bounds
+// Near memory's rate only while an element costs no more than some 15 vector operations: hence the decisions in float32, the bounds
 // as packed integers, and 16 elements a lane beside what a group costs once.
 template <typename T, int LANES, int TOKENS>
 __global__ __launch_bounds__(kThreads) void write_kernel(Kv4MoveArgs a, CHeads k, CHeads v) {

@@ -12,7 +12,7 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLargestFloat = 3.402823466e38f;
 constexpr float kNothing = -kLargestFloat;  // the reference of a row that has seen nothing
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kAlign = 32;  // cached tokens are taken in aligned runs of this many
 
 // Rows of one key head: row r of a sequence is its new token r / group and query head r % group of the key head's.
@@ -150,7 +150,8 @@ __device__ __forceinline__ void for_pieces(const AttnArgs& a, int* lds, F take) 
   if constexpr (!SPLIT) {
     const int tile = (int)(blockIdx.z * kGridTiles + blockIdx.y);
     if (tile >= a.n_tiles) return;
-    // the last tiles of causal rows see the most: all key heads' go first
+    // the last tiles of a causal sequence see the most: they go before its others, of all key heads (sequences in turn, the last one
+    // first, whatever their lengths)
     const RowTile t = row_tile(a, a.n_tiles - 1 - tile);
     const KvSpan s = kv_span(a, t);
     if (s.units) take(t, (int)blockIdx.x, s.begin, s.end, -1);

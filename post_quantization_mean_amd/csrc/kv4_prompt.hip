@@ -18,8 +18,9 @@
 //
 // 4096 tokens of 64 heads on 8 of 128 behind 8192: 1.47 - 1.54 ms (890 - 930 TFLOP/s; a large float16 library product reaches 1130
 // on this card). 4096 causal tokens of 32 heads with their own keys: 175 us (785). 9 prompts of up to 1500 tokens, 32 heads on 8
-// of 64: 102 us; heads of 64 have half the products for each exponential (4 x 2048 tokens behind 2048: 300 us, 690 TFLOP/s;
-// as two blocks of four waves a compute unit 338, the prompts alike), heads of 256 one wave a SIMD (540).
+// of 64: 105 us; heads of 64 have half the products for each exponential (4 x 2048 tokens behind 2048: 305 us, 675 TFLOP/s;
+// as two blocks of four waves a compute unit 338, the prompts alike), heads of 256 one wave a SIMD (535). Heads of 32 run as 64, of 96
+// as 128, of 160 to 224 as 256, with products of zeros (4096 tokens of 32 heads of 96 173 us, of 128 171).
 #include <type_traits>
 
 #include "kv4_device.h"
