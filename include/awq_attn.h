@@ -128,9 +128,10 @@ AWQ_API size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seq
  *   out        [n_tokens, n_heads, head_dim] of out_dtype (q_dtype or AWQ_DTYPE_F32). May be q, of the same type and pitches.
  *   lse        float32 [n_tokens, n_heads], contiguous, or NULL.
  * Products and sums are held in float32. Queries, the cache's numbers (keys only where a key head has many rows) and the
- * softmax's numerators (of float16 queries only there, too) are rounded to float16 for the matrix units (queries by way
- * of a power of two of each row, float16 ones only where a key head has few rows). A seen number of the cache past float16's largest counts there as +-65504 (awq_kv4_write
- * writes none); what a row does not see has no influence on it, whatever the memory holds. */
+ * softmax's numerators (of float16 queries only there, too) are rounded to float16 for the matrix units (queries by way of a
+ * power of two of each row, float16 ones only where a key head has few rows). A seen number of the cache past float16's
+ * largest counts there as +-65504 (awq_kv4_write writes none); what a row does not see has no influence on it, whatever the
+ * memory holds. */
 AWQ_API int awq_kv4_attention(const void* q, int64_t ld_q, int64_t ld_q_head, int q_dtype, int64_t n_tokens, int64_t n_heads,
                               int64_t n_kv, int64_t head_dim, const uint8_t* codes, int64_t page_codes, const void* params,
                               int64_t page_params, int64_t n_pages, int page_size, const int32_t* table, int64_t ld_table,
